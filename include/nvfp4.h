@@ -69,8 +69,11 @@ typedef enum {
   NVFP4_ERR_NONFINITE_INPUT = 5,    /* device: amax of an input is Inf/NaN */
   NVFP4_ERR_TIMEOUT = 6,            /* device: a bounded wait ran out */
   NVFP4_ERR_TOO_LARGE = 7,          /* input larger than nvfp4_quantize_noalloc's static scratch */
-  NVFP4_ERR_BOUNDS = 8              /* device, bounds-checking build only: a computed global index
+  NVFP4_ERR_BOUNDS = 8,             /* device, bounds-checking build only: a computed global index
                                        fell outside its buffer; that access was skipped */
+  NVFP4_ERR_PAGE = 9,               /* device, KV cache: an index, offset or length outside its cache, table
+                                       or pool; that part was skipped */
+  NVFP4_ERR_NO_PAGES = 10           /* device, KV cache: too few free pages; nothing was changed */
 } nvfp4_status;
 
 typedef enum {
@@ -320,6 +323,136 @@ nvfp4_status nvfp4_moe_workspace_layout(int64_t T, int64_t H, int64_t I, int E, 
 nvfp4_status nvfp4_quantize_noalloc(const void* x, int64_t M, int64_t K, nvfp4_mode mode,
                                     const float* g_in, uint8_t* codes, uint8_t* scales,
                                     float* g_out, uint8_t* fos_choice, nvfp4_stream_t stream);
+
+/*
+ * Paged NVFP4 KV cache ("Developing Nemotron 3.5 Lightning NVFP4 with QAD using
+ * NVIDIA Model Optimizer", Table 1 "four_over_six + NVFP4 KV": K and V stored
+ * in NVFP4, attention in 16-bit floating point, Q not quantized). The page does
+ * not describe a cache's pages; their layout and management are this library's.
+ *
+ * pages        [num_pages][kv_heads][nvfp4_kv_page_bytes(page_size, D)] bytes,
+ *              one layer's K and V. A (page, head) is page_size/16 granules of
+ *              16 tokens, each 18*D bytes: K codes [16][D/2] (element 2j in the
+ *              low nibble of byte j), K block scales [16][D/16] (E4M3), V
+ *              codes, V block scales. D = 64 or 128; page_size = 16, 32, 64 or
+ *              128.
+ * k_g, v_g     device FP32 scalars: static global scales of K and V.
+ * block_table  [batch][table_width] int32: page j of sequence b.
+ * cu_q         [batch + 1] int32, non-decreasing: rows [cu_q[b], cu_q[b+1]) of
+ *              the new-token tensors belong to sequence b.
+ * kv_len       [batch] int32: cached tokens of b, the new ones included. New
+ *              token i of n sits at position kv_len[b] - n + i.
+ * Lengths, offsets and tables are read on the device when the kernels run, so a
+ * captured graph can be replayed with other values. A negative, decreasing or
+ * too large offset or length, or a page outside the pool, is recorded as
+ * NVFP4_ERR_PAGE and its tokens are skipped (appending) or masked (attention).
+ * Rows at or behind cu_q[batch] are neither read nor written.
+ */
+
+/* Bytes of one head's part of a page; 0 for an unsupported size. Host only. */
+size_t nvfp4_kv_page_bytes(int page_size, int head_dim);
+
+/*
+ * nvfp4_kv_append -- quantize the new tokens' K and V into their pages, by the
+ *   arithmetic of nvfp4_quantize with g_in = k_g / v_g (modes MAX and
+ *   FOUR_OVER_SIX), bit for bit.
+ * k, v        BF16 [total][kv_heads][head_dim], 16-byte aligned, rows
+ *             row_stride elements apart (a multiple of 8, at least
+ *             kv_heads * head_dim: K and V may be parts of one projection).
+ * Device status: NVFP4_ERR_NONFINITE_INPUT for a block that holds Inf or NaN
+ * (zeros are stored), NVFP4_ERR_PAGE as above.
+ */
+nvfp4_status nvfp4_kv_append(const void* k, const void* v, int64_t row_stride, int64_t total,
+                             int kv_heads, int head_dim, const int32_t* cu_q, const int32_t* kv_len,
+                             int batch, const int32_t* block_table, int table_width, uint8_t* pages,
+                             int64_t num_pages, int page_size, const float* k_g, const float* v_g,
+                             nvfp4_mode mode, nvfp4_stream_t stream);
+
+/* Workspace bytes of nvfp4_paged_attention. Zero-fill it once before its first
+ * use; every call leaves it ready for the next. Calls that share one must be
+ * ordered on the GPU. Host only. */
+size_t nvfp4_paged_attention_workspace_bytes(void);
+
+/*
+ * nvfp4_paged_attention -- attention of the new tokens over the cached ones:
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k[j]) v[j] over the cached
+ *   tokens j that t sees: j < kv_len, j <= position of t if causal, position of
+ *   t - j < window if window > 0. Query head h reads KV head
+ *   h / (q_heads / kv_heads). Products of FP16 operands (cached values exact,
+ *   queries exact to 2^-29 of their row's largest, softmax weights rounded to
+ *   FP16), sums and softmax statistics in FP32, out rounded once to BF16.
+ * q           BF16 [total][q_heads][head_dim], 16-byte aligned, rows q_stride
+ *             elements apart (a multiple of 8).
+ * max_q       the most new tokens of any sequence, as the caller knows it: it
+ *             chooses the kernel and does not change what is computed (0 =
+ *             unknown).
+ * out         BF16 [total][q_heads][head_dim]; must not overlap q. A token that
+ *             sees nothing gets zeros.
+ * lse         nullable FP32 [total][q_heads]: log sum_j exp(scale * q . k), or
+ *             -Inf where a token sees nothing.
+ * Requirements: q_heads a multiple of kv_heads, at most 128 times it; scale
+ * positive and finite.
+ */
+nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_stride, int64_t total, int q_heads,
+                                   int kv_heads, int head_dim, const int32_t* cu_q,
+                                   const int32_t* kv_len, int batch, const int32_t* block_table,
+                                   int table_width, const uint8_t* pages, int64_t num_pages,
+                                   int page_size, const float* k_g, const float* v_g, float scale,
+                                   int causal, int64_t window, int64_t max_q, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * Page management. The pool's state, all on the device:
+ *   refs        [num_pages] int32: slots that hold a page; 0 = free.
+ *   block_table [slots][table_width] int32; seq_len [slots] int32: tokens held.
+ *   A slot holds ceil(seq_len / page_size) pages.
+ * The calls below change this state and name the pages whose contents have to
+ * move; nvfp4_kv_copy_pages then moves them, once for each layer's pages.
+ */
+
+/* Copy page src[i] to page dst[i] of one layer, i < n. Entries with a negative
+ * index are skipped. The dst pages must be distinct and none may be a src of the
+ * same call. page_bytes = kv_heads * nvfp4_kv_page_bytes (a multiple of 16). */
+nvfp4_status nvfp4_kv_copy_pages(uint8_t* pages, int64_t num_pages, int64_t page_bytes,
+                                 const int32_t* src, const int32_t* dst, int64_t n,
+                                 nvfp4_stream_t stream);
+
+/*
+ * nvfp4_kv_fork -- slot child[i] becomes a copy of slot parent[i], i < n: full
+ *   pages are shared (refs + 1); a part page gets a page of its own, the lowest
+ *   free ones in the order of i. src[i], dst[i]: the part page and the child's
+ *   page (copy them), -1 where there is none, -2 where the entry was refused:
+ *   a slot out of range, parent == child, a child that holds tokens or that an
+ *   earlier entry names (NVFP4_ERR_PAGE). With too few free pages nothing
+ *   changes, every src and dst is -2 and the device status NVFP4_ERR_NO_PAGES.
+ *   A child's tokens at or behind its parent's are not set in block_table.
+ */
+nvfp4_status nvfp4_kv_fork(int32_t* refs, int64_t num_pages, int32_t* block_table, int slots,
+                           int table_width, int32_t* seq_len, int page_size, const int32_t* parent,
+                           const int32_t* child, int n, int32_t* src, int32_t* dst,
+                           nvfp4_stream_t stream);
+
+/* Free the slots which[i], i < n: their pages' refs - 1, their entries of
+ * block_table -1, seq_len 0. A slot named twice is freed once. */
+nvfp4_status nvfp4_kv_free(int32_t* refs, int64_t num_pages, int32_t* block_table, int slots,
+                           int table_width, int32_t* seq_len, int page_size, const int32_t* which,
+                           int n, nvfp4_stream_t stream);
+
+/* Workspace bytes of nvfp4_kv_compact (no initialisation needed). Host only. */
+size_t nvfp4_kv_compact_workspace_bytes(int64_t num_pages);
+
+/*
+ * nvfp4_kv_compact -- bring the L used pages to indices 0..L-1: the i-th used
+ *   page at or above L moves to the i-th free page below L, both in ascending
+ *   order. refs_out, table_out: the state after the moves (each may be its input
+ *   itself). src, dst [max(1, num_pages / 2)]: the moves in order, then -1.
+ *   live: L. Copy the pages before anything reads them by the new table.
+ */
+nvfp4_status nvfp4_kv_compact(const int32_t* refs, int64_t num_pages, const int32_t* block_table,
+                              int slots, int table_width, const int32_t* seq_len, int page_size,
+                              int32_t* refs_out, int32_t* table_out, int32_t* src, int32_t* dst,
+                              int32_t* live, void* workspace, size_t workspace_bytes,
+                              nvfp4_stream_t stream);
 
 /* Conversion primitives (diagnostics; the quantize kernels use the same
  * device code). e2m1: code of each FP32 value, one per byte, RNE, saturate

@@ -21,6 +21,8 @@ __all__ = [
     "moe_workspace_layout", "convert_e2m1", "convert_e4m3", "device_status", "selftest_timeout",
     "quantize_workspace_bytes", "moe_workspace_bytes", "quantize_experts", "quantize_noalloc",
     "selftest_gemm_timeout", "kernel_launches", "probe_mma_peak",
+    "KVCache", "kv_cache", "kv_page_bytes", "kv_append", "paged_attention", "kv_copy_pages", "kv_fork", "kv_free",
+    "kv_compact",
 ]
 
 MODE_MAX = 0
@@ -39,7 +41,9 @@ library_path = (os.path.join(_HERE, "libnvfp4_debug.so") if _choice == "debug"
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported device", 3: "CUDA error",
            4: "workspace missing or too small", 5: "non-finite input", 6: "device wait timed out",
            7: "input too large for the no-alloc entry point (M*K > 2^30)",
-           8: "index outside its buffer (bounds-checking build)"}
+           8: "index outside its buffer (bounds-checking build)",
+           9: "KV cache: an index, offset or length outside its cache, table or pool",
+           10: "KV cache: too few free pages"}
 
 
 class NVFP4Error(RuntimeError):
@@ -57,6 +61,7 @@ class _MoeLayout(ctypes.Structure):
 _lib = None
 _lib_lock = threading.Lock()
 P, I64, I32, SZ, U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
+F32 = ctypes.c_float
 
 _SIGS = {
     "nvfp4_version": (I32, []),
@@ -74,6 +79,16 @@ _SIGS = {
     "nvfp4_moe_workspace_bytes": (SZ, [I64, I64, I64, I32, I32]),
     "nvfp4_moe_grouped_gemm": (I32, [P, I64, I64, P, P, I32, I32, I64, P, P, P, P, P, P, P, P, SZ, P]),
     "nvfp4_moe_workspace_layout": (I32, [I64, I64, I64, I32, I32, ctypes.POINTER(_MoeLayout)]),
+    "nvfp4_kv_page_bytes": (SZ, [I32, I32]),
+    "nvfp4_paged_attention_workspace_bytes": (SZ, []),
+    "nvfp4_kv_compact_workspace_bytes": (SZ, [I64]),
+    "nvfp4_kv_append": (I32, [P, P, I64, I64, I32, I32, P, P, I32, P, I32, P, I64, I32, P, P, I32, P]),
+    "nvfp4_paged_attention": (I32, [P, I64, I64, I32, I32, I32, P, P, I32, P, I32, P, I64, I32, P, P, F32, I32, I64,
+                                    I64, P, P, P, SZ, P]),
+    "nvfp4_kv_copy_pages": (I32, [P, I64, I64, P, P, I64, P]),
+    "nvfp4_kv_fork": (I32, [P, I64, P, I32, I32, P, I32, P, P, I32, P, P, P]),
+    "nvfp4_kv_free": (I32, [P, I64, P, I32, I32, P, I32, P, I32, P]),
+    "nvfp4_kv_compact": (I32, [P, I64, P, I32, I32, P, I32, P, P, P, P, P, P, SZ, P]),
     "nvfp4_convert_e2m1": (I32, [P, I64, P, P]),
     "nvfp4_convert_e4m3": (I32, [P, I64, P, P]),
     "nvfp4_get_device_status": (I32, [P, I32, ctypes.POINTER(ctypes.c_int)]),
@@ -371,6 +386,221 @@ def moe_grouped_gemm(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tens
                                       _stream(dev))
     _check(st, "nvfp4_moe_grouped_gemm")
     return out, workspace
+
+
+class KVCache(NamedTuple):
+    """One layer's paged NVFP4 K and V: ``pages`` uint8 [num_pages, kv_heads,
+    kv_page_bytes(page_size, head_dim)] (layout in include/nvfp4.h) and the
+    static FP32 global scales of K and V (1-element device tensors)."""
+    pages: torch.Tensor
+    k_g: torch.Tensor
+    v_g: torch.Tensor
+    page_size: int
+    head_dim: int
+
+
+def kv_page_bytes(page_size: int, head_dim: int) -> int:
+    """Bytes of one head's part of a page; 0 for sizes without a kernel."""
+    return int(lib().nvfp4_kv_page_bytes(page_size, head_dim))
+
+
+def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int, k_g: torch.Tensor,
+             v_g: torch.Tensor) -> KVCache:
+    """An empty (zero-filled) cache on the device of ``k_g``; ``k_g`` and
+    ``v_g`` are the calibrated amax / 2688 of K and V."""
+    nbytes = kv_page_bytes(page_size, head_dim)
+    if nbytes == 0:
+        raise ValueError("page_size must be 16, 32, 64 or 128 and head_dim 64 or 128")
+    pages = torch.zeros((num_pages, kv_heads, nbytes), dtype=torch.uint8, device=k_g.device)
+    return KVCache(pages, k_g, v_g, page_size, head_dim)
+
+
+def _ints(t: torch.Tensor, name: str, dev: torch.device, *shape) -> int:
+    """Checks a contiguous int32 tensor on dev (None in shape: any size); returns its address."""
+    if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous torch.int32 tensor on {dev}")
+    if t.dim() != len(shape) or any(want is not None and want != got for want, got in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(x: torch.Tensor, name: str, dev: torch.device, heads: Optional[int], dim: int) -> int:
+    """Checks BF16 [tokens, heads, dim] whose tokens are contiguous (a part of a
+    projection's output is); returns the elements from one token to the next."""
+    if x.dtype != torch.bfloat16 or x.device != dev or x.dim() != 3:
+        raise ValueError(f"{name} must be a torch.bfloat16 [tokens, heads, head_dim] tensor on {dev}")
+    n, h, d = x.shape
+    if d != dim or (heads is not None and h != heads) or h == 0:
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim}], got {list(x.shape)}")
+    stride = x.stride()
+    if stride[2] != 1 or (h > 1 and stride[1] != d):
+        raise ValueError(f"{name}: the values of a token must be contiguous")
+    return stride[0] if n > 1 else h * d
+
+
+def _kv_cache_of(cache: KVCache):
+    """Checks a cache; returns (device, pages, kv heads)."""
+    pages = cache.pages
+    if pages.dim() != 3 or pages.dtype != torch.uint8 or not pages.is_cuda or not pages.is_contiguous():
+        raise ValueError("cache.pages must be a contiguous uint8 CUDA tensor [num_pages, kv_heads, page bytes]")
+    dev = pages.device
+    nbytes = kv_page_bytes(cache.page_size, cache.head_dim)
+    if nbytes == 0 or pages.shape[2] != nbytes:
+        raise ValueError(f"cache.pages does not fit page_size {cache.page_size} and head_dim {cache.head_dim}")
+    for g in (cache.k_g, cache.v_g):
+        if g.dtype != torch.float32 or g.numel() != 1 or g.device != dev:
+            raise ValueError("cache.k_g and cache.v_g must be 1-element FP32 tensors on the cache's device")
+    return dev, pages.shape[0], pages.shape[1]
+
+
+# The attention's workspace holds counters that are zero between calls. One per
+# (device, stream) outside of graph capture; a captured call takes one of its
+# own from the graph's memory, zeroed by the graph, so that graphs replayed at
+# the same time, and eager calls beside them, share nothing.
+_attn_ws: dict = {}
+
+
+def _attention_workspace(dev: torch.device) -> torch.Tensor:
+    nbytes = int(lib().nvfp4_paged_attention_workspace_bytes())
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+    stream = torch.cuda.current_stream(dev)
+    key = (dev.index, stream.cuda_stream)
+    with _ws_lock:
+        entry = _attn_ws.get(key)
+        if entry is None:
+            entry = _attn_ws[key] = (stream, torch.zeros(nbytes, dtype=torch.uint8, device=dev))
+    return entry[1]
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, cu_q: torch.Tensor,
+              kv_len: torch.Tensor, mode="max") -> None:
+    """Quantize the new tokens' K and V (BF16 [tokens, kv_heads, head_dim]) into
+    the cache's pages (nvfp4_kv_append). ``cu_q`` [batch+1]: first row of each
+    sequence; ``kv_len`` [batch]: cached tokens, the new ones included;
+    ``block_table`` [batch, width]: pages of each sequence (all int32)."""
+    dev, num_pages, heads = _kv_cache_of(cache)
+    stride = _rows(k, "k", dev, heads, cache.head_dim)
+    if _rows(v, "v", dev, heads, cache.head_dim) != stride or v.shape != k.shape:
+        raise ValueError("k and v must have the same shape and strides")
+    batch = kv_len.shape[0]
+    args = (_ints(cu_q, "cu_q", dev, batch + 1), _ints(kv_len, "kv_len", dev, batch), batch,
+            _ints(block_table, "block_table", dev, batch, None), block_table.shape[1])
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_kv_append(k.data_ptr(), v.data_ptr(), stride, k.shape[0], heads, cache.head_dim, *args,
+                                   cache.pages.data_ptr(), num_pages, cache.page_size, cache.k_g.data_ptr(),
+                                   cache.v_g.data_ptr(), _MODES[mode], _stream(dev))
+    _check(st, "nvfp4_kv_append")
+
+
+def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
+                    kv_len: torch.Tensor, scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                    max_q: Optional[int] = None, want_lse: bool = False, out: Optional[torch.Tensor] = None,
+                    lse_out: Optional[torch.Tensor] = None):
+    """Attention of the new tokens' queries (BF16 [tokens, q_heads, head_dim])
+    over the paged NVFP4 cache (nvfp4_paged_attention). ``scale`` defaults to
+    head_dim ** -0.5; ``window`` > 0 limits a token to the last ``window``
+    positions; ``max_q``: the most new tokens of a sequence, if known (it
+    chooses the kernel only). Returns (out BF16, lse FP32 [tokens, q_heads] or
+    None)."""
+    dev, num_pages, heads = _kv_cache_of(cache)
+    dim = cache.head_dim
+    stride = _rows(q, "q", dev, None, dim)
+    total, hq = q.shape[:2]
+    batch = kv_len.shape[0]
+    args = (_ints(cu_q, "cu_q", dev, batch + 1), _ints(kv_len, "kv_len", dev, batch), batch,
+            _ints(block_table, "block_table", dev, batch, None), block_table.shape[1])
+    if out is None:
+        out = torch.empty((total, hq, dim), dtype=torch.bfloat16, device=dev)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous torch.bfloat16 {list(q.shape)} tensor on {dev}")
+    if want_lse and lse_out is None:
+        lse_out = torch.empty((total, hq), dtype=torch.float32, device=dev)
+    elif lse_out is not None and (lse_out.shape != (total, hq) or lse_out.dtype != torch.float32 or
+                                  lse_out.device != dev or not lse_out.is_contiguous()):
+        raise ValueError(f"lse_out must be a contiguous torch.float32 [{total}, {hq}] tensor on {dev}")
+    if max_q is None:
+        max_q = 1 if total <= batch else 0
+    with torch.cuda.device(dev):
+        ws = _attention_workspace(dev)
+        st = lib().nvfp4_paged_attention(q.data_ptr(), stride, total, hq, heads, dim, *args, cache.pages.data_ptr(),
+                                         num_pages, cache.page_size, cache.k_g.data_ptr(), cache.v_g.data_ptr(),
+                                         dim ** -0.5 if scale is None else scale, int(causal), window, max_q,
+                                         out.data_ptr(), None if lse_out is None else lse_out.data_ptr(),
+                                         ws.data_ptr(), ws.numel(), _stream(dev))
+    _check(st, "nvfp4_paged_attention")
+    return out, lse_out
+
+
+def kv_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Copy page src[i] to page dst[i] (int32; negative: skipped). The dst pages
+    are distinct and none of them is a src (nvfp4_kv_copy_pages)."""
+    dev, num_pages, heads = _kv_cache_of(cache)
+    n = src.shape[0]
+    args = _ints(src, "src", dev, n), _ints(dst, "dst", dev, n), n
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_kv_copy_pages(cache.pages.data_ptr(), num_pages, heads * cache.pages.shape[2], *args,
+                                       _stream(dev))
+    _check(st, "nvfp4_kv_copy_pages")
+
+
+def _pool(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor, page_size: int):
+    """Checks a pool's state; returns (device, the C calls' leading arguments)."""
+    if not refs.is_cuda:
+        raise ValueError("refs must be a CUDA tensor")
+    dev = refs.device
+    slots = seq_len.shape[0]
+    return dev, (_ints(refs, "refs", dev, None), refs.shape[0], _ints(block_table, "block_table", dev, slots, None),
+                 slots, block_table.shape[1], _ints(seq_len, "seq_len", dev, slots), page_size)
+
+
+def kv_fork(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor, parent: torch.Tensor,
+            child: torch.Tensor, page_size: int):
+    """Make slot child[i] a copy of slot parent[i] (nvfp4_kv_fork). Updates the
+    pool's state and returns (src, dst): the part pages to copy with
+    kv_copy_pages, in every layer's cache."""
+    dev, pool = _pool(refs, block_table, seq_len, page_size)
+    n = parent.shape[0]
+    args = _ints(parent, "parent", dev, n), _ints(child, "child", dev, n), n
+    src, dst = torch.empty((2, n), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_kv_fork(*pool, *args, src.data_ptr(), dst.data_ptr(), _stream(dev))
+    _check(st, "nvfp4_kv_fork")
+    return src, dst
+
+
+def kv_free(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor, slots: torch.Tensor,
+            page_size: int) -> None:
+    """Free the named slots (nvfp4_kv_free)."""
+    dev, pool = _pool(refs, block_table, seq_len, page_size)
+    n = slots.shape[0]
+    which = _ints(slots, "slots", dev, n)
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_kv_free(*pool, which, n, _stream(dev))
+    _check(st, "nvfp4_kv_free")
+
+
+def kv_compact(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor, page_size: int,
+               refs_out: Optional[torch.Tensor] = None, table_out: Optional[torch.Tensor] = None):
+    """Bring the used pages to the lowest indices (nvfp4_kv_compact). Returns
+    (refs, block_table, src, dst, live): the state after the moves (new tensors
+    unless refs_out / table_out are given, which may be the inputs), the moves
+    for kv_copy_pages (-1 behind the last) and the number of used pages [1]."""
+    dev, pool = _pool(refs, block_table, seq_len, page_size)
+    pages = refs.shape[0]
+    refs_out = torch.empty_like(refs) if refs_out is None else refs_out
+    table_out = torch.empty_like(block_table) if table_out is None else table_out
+    outs = _ints(refs_out, "refs_out", dev, pages), _ints(table_out, "table_out", dev, *block_table.shape)
+    cap = max(1, pages // 2)
+    src, dst = torch.empty((2, cap), dtype=torch.int32, device=dev)
+    live = torch.empty(1, dtype=torch.int32, device=dev)
+    nbytes = int(lib().nvfp4_kv_compact_workspace_bytes(pages))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_kv_compact(*pool, *outs, src.data_ptr(), dst.data_ptr(), live.data_ptr(), ws.data_ptr(),
+                                    nbytes, _stream(dev))
+    _check(st, "nvfp4_kv_compact")
+    return refs_out, table_out, src, dst, live
 
 
 def convert_e2m1(v: torch.Tensor) -> torch.Tensor:

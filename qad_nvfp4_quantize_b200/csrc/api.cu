@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "kv_attention.cuh"
 
 namespace {
 
@@ -52,6 +53,21 @@ nvfp4_status current_device(DeviceInfo** out) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 nvfp4_status launched(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
+
+// Shapes of the paged KV cache: whole granules, head sizes with a kernel.
+bool kv_shape_ok(int page_size, int head_dim) {
+  return (page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128) &&
+         (head_dim == 64 || head_dim == 128);
+}
+bool kv_sizes_ok(int64_t total, int kv_heads, int batch, int table_width, int64_t num_pages, int page_size) {
+  return total >= 0 && total < (int64_t(1) << 31) && kv_heads > 0 && kv_heads <= 1024 && batch >= 0 &&
+         batch < (1 << 24) && table_width >= 0 && (int64_t)table_width * page_size < (int64_t(1) << 31) &&
+         num_pages >= 0 && num_pages < (int64_t(1) << 31);
+}
+bool pool_ok(int64_t num_pages, int slots, int table_width, int page_size) {
+  return num_pages >= 0 && num_pages < (int64_t(1) << 31) - (1 << 16) && slots >= 0 && table_width >= 0 &&
+         page_size >= 1 && (int64_t)table_width * page_size < (int64_t(1) << 31) && table_width <= (1 << 23);
+}
 
 // Dynamic global scale: amax pass 1 into the workspace.
 nvfp4_status run_amax(const void* x, int64_t n, void* ws, size_t ws_bytes, int num_sms, cudaStream_t s,
@@ -101,6 +117,8 @@ const char* nvfp4_status_string(nvfp4_status s) {
     case NVFP4_ERR_TIMEOUT: return "device wait timed out";
     case NVFP4_ERR_TOO_LARGE: return "input larger than the no-alloc entry point's static scratch (M*K > 2^30)";
     case NVFP4_ERR_BOUNDS: return "a computed index fell outside its buffer (bounds-checking build)";
+    case NVFP4_ERR_PAGE: return "KV cache: an index, offset or length outside its cache, table or pool";
+    case NVFP4_ERR_NO_PAGES: return "KV cache: too few free pages";
   }
   return "unknown status";
 }
@@ -256,6 +274,134 @@ nvfp4_status nvfp4_fake_quant_backward(const void* x, const void* grad_y, int64_
   }
   return launched(nvfp4::launch_fake_quant_bwd(x, grad_y, M, K, fos, partial, np, g_frozen, scales_frozen, grad_x,
                                                d->status, d->num_sms, s));
+}
+
+size_t nvfp4_kv_page_bytes(int page_size, int head_dim) {
+  if (!kv_shape_ok(page_size, head_dim)) return 0;
+  return (size_t)(page_size / nvfp4::kGranule) * nvfp4::granule_bytes(head_dim);
+}
+
+size_t nvfp4_paged_attention_workspace_bytes(void) { return nvfp4::kv_attention_workspace_bytes(); }
+
+size_t nvfp4_kv_compact_workspace_bytes(int64_t num_pages) {
+  return num_pages < 0 ? 0 : nvfp4::kv_compact_workspace_bytes(num_pages);
+}
+
+nvfp4_status nvfp4_kv_append(const void* k, const void* v, int64_t row_stride, int64_t total, int kv_heads,
+                             int head_dim, const int32_t* cu_q, const int32_t* kv_len, int batch,
+                             const int32_t* block_table, int table_width, uint8_t* pages, int64_t num_pages,
+                             int page_size, const float* k_g, const float* v_g, nvfp4_mode mode,
+                             nvfp4_stream_t stream) {
+  if (!kv_shape_ok(page_size, head_dim) || !kv_sizes_ok(total, kv_heads, batch, table_width, num_pages, page_size) ||
+      (mode != NVFP4_MODE_MAX && mode != NVFP4_MODE_FOUR_OVER_SIX))
+    return NVFP4_ERR_INVALID_ARG;
+  if (row_stride % 8 || row_stride < (int64_t)kv_heads * head_dim) return NVFP4_ERR_INVALID_ARG;
+  if (total > 0 && batch > 0 &&
+      (!k || !v || !cu_q || !kv_len || !block_table || !pages || !k_g || !v_g || !aligned16(k) || !aligned16(v) ||
+       !aligned16(pages)))
+    return NVFP4_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  nvfp4_status st = current_device(&d);
+  if (st != NVFP4_OK) return st;
+  const nvfp4::KvIndex ix{cu_q, kv_len, block_table, batch, table_width, page_size, kv_heads, total, num_pages};
+  return launched(nvfp4::launch_kv_append(k, v, row_stride, head_dim, ix, pages, k_g, v_g,
+                                          mode == NVFP4_MODE_FOUR_OVER_SIX, d->status, d->num_sms,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_stride, int64_t total, int q_heads, int kv_heads,
+                                   int head_dim, const int32_t* cu_q, const int32_t* kv_len, int batch,
+                                   const int32_t* block_table, int table_width, const uint8_t* pages,
+                                   int64_t num_pages, int page_size, const float* k_g, const float* v_g, float scale,
+                                   int causal, int64_t window, int64_t max_q, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, nvfp4_stream_t stream) {
+  if (!kv_shape_ok(page_size, head_dim) || !kv_sizes_ok(total, kv_heads, batch, table_width, num_pages, page_size))
+    return NVFP4_ERR_INVALID_ARG;
+  if (q_heads <= 0 || q_heads % kv_heads || q_heads / kv_heads > 128) return NVFP4_ERR_INVALID_ARG;
+  if (total * (q_heads / kv_heads) >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || scale > 3.0e38f || window < 0 || max_q < 0) return NVFP4_ERR_INVALID_ARG;
+  if (q_stride % 8 || q_stride < (int64_t)q_heads * head_dim) return NVFP4_ERR_INVALID_ARG;
+  if (total > 0 && batch > 0) {
+    if (!q || !cu_q || !kv_len || !block_table || !pages || !k_g || !v_g || !out || !aligned16(q) ||
+        !aligned16(pages) || !aligned16(out) || q == out)
+      return NVFP4_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < nvfp4::kv_attention_workspace_bytes() || !aligned16(workspace))
+      return NVFP4_ERR_WORKSPACE;
+  }
+  DeviceInfo* d;
+  nvfp4_status st = current_device(&d);
+  if (st != NVFP4_OK) return st;
+  nvfp4::AttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.ix = nvfp4::KvIndex{cu_q, kv_len, block_table, batch, table_width, page_size, kv_heads, total, num_pages};
+  a.pages = pages;
+  a.k_g = k_g;
+  a.v_g = v_g;
+  a.scale = scale;
+  a.group = q_heads / kv_heads;
+  a.causal = causal != 0;
+  a.window = window;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.status = d->status;
+  return launched(nvfp4::launch_kv_attention(a, head_dim, max_q, workspace, d->num_sms,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_kv_copy_pages(uint8_t* pages, int64_t num_pages, int64_t page_bytes, const int32_t* src,
+                                 const int32_t* dst, int64_t n, nvfp4_stream_t stream) {
+  if (num_pages < 0 || page_bytes <= 0 || page_bytes % 16 || page_bytes > (int64_t(1) << 30) || n < 0 ||
+      n >= (int64_t(1) << 31))
+    return NVFP4_ERR_INVALID_ARG;
+  if (n > 0 && (!pages || !src || !dst || !aligned16(pages))) return NVFP4_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  nvfp4_status st = current_device(&d);
+  if (st != NVFP4_OK) return st;
+  return launched(nvfp4::launch_kv_copy(pages, num_pages, page_bytes, src, dst, n, d->status, d->num_sms,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_kv_fork(int32_t* refs, int64_t num_pages, int32_t* block_table, int slots, int table_width,
+                           int32_t* seq_len, int page_size, const int32_t* parent, const int32_t* child, int n,
+                           int32_t* src, int32_t* dst, nvfp4_stream_t stream) {
+  if (!pool_ok(num_pages, slots, table_width, page_size) || n < 0 || n > (1 << 20)) return NVFP4_ERR_INVALID_ARG;
+  if (n > 0 && (!refs || !block_table || !seq_len || !parent || !child || !src || !dst || src == dst))
+    return NVFP4_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  nvfp4_status st = current_device(&d);
+  if (st != NVFP4_OK) return st;
+  const nvfp4::PoolArgs a{refs, block_table, seq_len, num_pages, slots, table_width, page_size};
+  return launched(nvfp4::launch_kv_fork(a, parent, child, n, src, dst, d->status,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_kv_free(int32_t* refs, int64_t num_pages, int32_t* block_table, int slots, int table_width,
+                           int32_t* seq_len, int page_size, const int32_t* which, int n, nvfp4_stream_t stream) {
+  if (!pool_ok(num_pages, slots, table_width, page_size) || n < 0) return NVFP4_ERR_INVALID_ARG;
+  if (n > 0 && (!refs || !block_table || !seq_len || !which)) return NVFP4_ERR_INVALID_ARG;
+  DeviceInfo* d;
+  nvfp4_status st = current_device(&d);
+  if (st != NVFP4_OK) return st;
+  const nvfp4::PoolArgs a{refs, block_table, seq_len, num_pages, slots, table_width, page_size};
+  return launched(nvfp4::launch_kv_free(a, which, n, d->status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_kv_compact(const int32_t* refs, int64_t num_pages, const int32_t* block_table, int slots,
+                              int table_width, const int32_t* seq_len, int page_size, int32_t* refs_out,
+                              int32_t* table_out, int32_t* src, int32_t* dst, int32_t* live, void* workspace,
+                              size_t workspace_bytes, nvfp4_stream_t stream) {
+  if (!pool_ok(num_pages, slots, table_width, page_size) || num_pages < 1) return NVFP4_ERR_INVALID_ARG;
+  if (!refs || !refs_out || !src || !dst || !live || src == dst) return NVFP4_ERR_INVALID_ARG;
+  if (slots > 0 && table_width > 0 && (!block_table || !table_out || !seq_len)) return NVFP4_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < nvfp4::kv_compact_workspace_bytes(num_pages)) return NVFP4_ERR_WORKSPACE;
+  DeviceInfo* d;
+  nvfp4_status st = current_device(&d);
+  if (st != NVFP4_OK) return st;
+  const nvfp4::PoolArgs a{const_cast<int32_t*>(refs), const_cast<int32_t*>(block_table),
+                          const_cast<int32_t*>(seq_len), num_pages, slots, table_width, page_size};
+  return launched(nvfp4::launch_kv_compact(a, refs_out, table_out, src, dst, live, workspace, d->status, d->num_sms,
+                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
 nvfp4_status nvfp4_get_device_status(nvfp4_stream_t stream, int clear, nvfp4_status* out) {

@@ -90,6 +90,29 @@ struct MoeArgs {
 int64_t moe_rows_capacity(int64_t T, int topk, int E);
 cudaError_t launch_moe(const MoeArgs& a, int* status, int num_sms, cudaStream_t s);
 
+// Paged NVFP4 KV cache (kv_append.cu, kv_pages.cu, kv_attention.cu).
+struct KvIndex;
+struct AttnArgs;
+cudaError_t launch_kv_append(const void* k, const void* v, int64_t stride, int D, const KvIndex& ix, uint8_t* pages,
+                             const float* k_g, const float* v_g, bool fos, int* status, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_attention(AttnArgs a, int D, int64_t max_q, void* workspace, int num_sms, cudaStream_t s);
+size_t kv_attention_workspace_bytes();
+struct PoolArgs {
+  int32_t* refs;
+  int32_t* table;
+  int32_t* seq_len;
+  int64_t num_pages;
+  int slots, width, page;
+};
+cudaError_t launch_kv_copy(uint8_t* pages, int64_t num_pages, int64_t page_bytes, const int32_t* src,
+                           const int32_t* dst, int64_t n, int* status, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_fork(const PoolArgs& a, const int32_t* parent, const int32_t* child, int n, int32_t* src,
+                           int32_t* dst, int* status, cudaStream_t s);
+cudaError_t launch_kv_free(const PoolArgs& a, const int32_t* which, int n, int* status, cudaStream_t s);
+size_t kv_compact_workspace_bytes(int64_t num_pages);
+cudaError_t launch_kv_compact(const PoolArgs& a, int32_t* refs_out, int32_t* table_out, int32_t* src, int32_t* dst,
+                              int32_t* live, void* workspace, int* status, int num_sms, cudaStream_t s);
+
 // Current device: the sm_100 gate, SM count and the address of the device
 // status word (api.cu). Returns NVFP4_OK or the gate's error code.
 int current_device_context(int* num_sms, int** status);

@@ -1,0 +1,610 @@
+// nvfp4_paged_attention for few query rows per KV head (decode, drafted
+// tokens): out = softmax(scale * Q K^T + mask) V over the paged NVFP4 cache.
+//
+// Mathematics: one pass over the cached tokens with a running maximum m, sum l
+// and unnormalised output O per query row: m' = max(m, s), O = O * 2^(m - m') +
+// 2^(s - m') v (scores in units of log2). O and l are rescaled only when a
+// score exceeds m by more than 8, so p = 2^(s - m) stays below 2^8 and the sum
+// in FP32 loses nothing.
+//
+// Bound: HBM, 18*D bytes per 16 tokens and KV head. The rows of one KV head
+// (all its query heads, all new tokens of the tile) share each fetched granule.
+//
+// Layout. S^T = K Q^T and O^T = V^T P^T with mma m16n8k16 (FP16 in, FP32 out):
+// tokens resp. head dimensions fill the 16 rows, so 8 query rows waste nothing
+// and the codes are dequantized straight into the A fragments, each exactly
+// once. (A 128-row tcgen05 tile needs 1024 tensor cycles per 128 tokens and
+// head; their bytes arrive in 805.) P^T moves from accumulator to B fragment
+// by two 8x8 transposes. The order of head dimensions and of tokens within an
+// MMA is free as long as both operands agree; it is chosen so that a lane's
+// codes are contiguous.
+//
+// Every warp works alone: granule i of a CTA's span goes to warp i mod 8, which
+// keeps kStages bulk copies of 18*D bytes in flight on its own barriers and its
+// own m, l, O; the warps meet at the end of the span. The spans come from
+// cutting the list of all granules of all (sequence, row tile, head) works into
+// equal parts, one per CTA, on the device, from the lengths as they are at run
+// time: ragged batches and graphs replayed with other lengths stay balanced. A
+// work cut by such a boundary leaves partial (m, l, O) in the workspace; the
+// last CTA that arrives at the work's counter joins the parts in index order
+// (no CTA waits, and the result does not depend on which one is last).
+#include <cuda_fp16.h>
+
+#include "kv_attention.cuh"
+
+namespace nvfp4 {
+
+constexpr int kAttnWarps = 8;
+constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr uint64_t kAttnWaitNs = 2000000000ull;
+constexpr float kRescaleAt = 8.0f;
+
+template <int D, int NT>
+struct AttnShared {
+  static constexpr int kStages = 5;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kPad = D + 8;  // row pitch of the joining buffer
+  union {
+    uint8_t ring[kAttnWarps][kStages][granule_bytes(D)];
+    float join[kAttnWarps][kRows][kPad];
+  };
+  uint64_t bar[kAttnWarps][kStages];
+  float wm[kAttnWarps][kRows], wl[kAttnWarps][kRows];
+  float m[kRows], l[kRows];
+  int64_t scan[kAttnWarps + 1];
+  int64_t found_base;
+  int found_b, last, abort;
+};
+
+NVFP4_DEVINL void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                            uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+NVFP4_DEVINL uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+NVFP4_DEVINL uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Token (within its granule) of MMA row or depth index i: a lane's four tokens
+// of V^T (depths 2t, 2t+1, 2t+8, 2t+9) and the rows of K that eight lanes fetch
+// together then fall into different shared-memory banks.
+__host__ __device__ constexpr int token_of(int i) {
+  return (i & 8) + ((i & 1) ? (((i & 7) >> 1) + 4) ^ 1 : (i & 7) >> 1);
+}
+
+// The granules that a row tile of a sequence needs: first granule and count
+// (0 when no row of the tile sees a token).
+struct Span {
+  int32_t g0, n;
+};
+template <int kRows>
+NVFP4_DEVINL Span tile_span(const AttnArgs& a, const KvSeq& s, int64_t tile) {
+  const int64_t r1 = (tile + 1) * kRows < (int64_t)s.rows * a.group ? (tile + 1) * kRows : (int64_t)s.rows * a.group;
+  const int64_t first = tile * kRows / a.group, last = (r1 - 1) / a.group, pos = (int64_t)s.len - s.rows;
+  const Visible v0 = visible(pos + first, s.len, a.causal, a.window);
+  const Visible v1 = visible(pos + last, s.len, a.causal, a.window);
+  if (v1.hi <= v0.lo) return Span{0, 0};
+  const int32_t g0 = v0.lo / kGranule;
+  return Span{g0, (v1.hi + kGranule - 1) / kGranule - g0};
+}
+// Work units of a tile for one head: its granules, at least one (an empty tile
+// still writes its rows).
+NVFP4_DEVINL int64_t units_of(const Span& s) { return s.n > 0 ? s.n : 1; }
+
+template <int kRows>
+NVFP4_DEVINL int64_t sequence_units(const AttnArgs& a, int b, int* status) {
+  const KvSeq s = kv_sequence(a.ix, b, status);
+  const int64_t tiles = ((int64_t)s.rows * a.group + kRows - 1) / kRows;
+  int64_t u = 0;
+  for (int64_t t = 0; t < tiles; ++t) u += units_of(tile_span<kRows>(a, s, t));
+  return u * a.ix.hkv;
+}
+
+// Exclusive scan over the CTA; total in *total.
+template <class Sh>
+NVFP4_DEVINL int64_t cta_scan(Sh& sh, int64_t v, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  __syncthreads();
+  if (lane == 31) sh.scan[warp] = incl;
+  __syncthreads();
+  int64_t pre = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kAttnWarps; ++w) {
+    const int64_t x = sh.scan[w];
+    pre += w < warp ? x : 0;
+    all += x;
+  }
+  *total = all;
+  return pre + incl - v;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_kernel(const AttnArgs a, int min_units) {
+  using Sh = AttnShared<D, NT>;
+  extern __shared__ __align__(128) uint8_t attn_smem[];
+  Sh& sh = *reinterpret_cast<Sh*>(attn_smem);
+  constexpr int kRows = Sh::kRows, kStages = Sh::kStages, kGB = granule_bytes(D);
+  constexpr int kSteps = D / 16;        // k-steps of S, m-tiles of O
+  constexpr int kWords = D / 32;        // code words per lane and K row
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int gpp = a.ix.page / kGranule;
+
+  if (lane == 0)
+    for (int i = 0; i < kStages; ++i) mbar_init(&sh.bar[warp][i], 1);
+  if (tid == 0) sh.abort = 0;
+  fence_barrier_init();
+
+  // ---- this CTA's span of the list of all units
+  int64_t total = 0;
+  {
+    int64_t mine = 0;
+    for (int b = tid; b < a.ix.batch; b += kAttnThreads) mine += sequence_units<kRows>(a, b, a.status);
+    cta_scan(sh, mine, &total);
+  }
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < min_units) per = min_units;
+  const int64_t u0 = per * blockIdx.x, u1 = u0 + per < total ? u0 + per : total;
+  if (u0 >= u1) return;
+  for (int64_t base = 0, b0 = 0;; b0 += kAttnThreads) {
+    const int b = (int)b0 + tid;
+    const int64_t v = b < a.ix.batch ? sequence_units<kRows>(a, b, nullptr) : 0;
+    int64_t sum;
+    const int64_t pre = base + cta_scan(sh, v, &sum);
+    if (u0 >= pre && u0 < pre + v) {
+      sh.found_b = b;
+      sh.found_base = pre;
+    }
+    base += sum;
+    if (u0 < base) break;
+  }
+  __syncthreads();
+  int b = sh.found_b;
+  int64_t base = sh.found_base, tile = 0;
+  KvSeq seq = kv_sequence(a.ix, b, nullptr);
+  Span span = tile_span<kRows>(a, seq, 0);
+  uint32_t phase = 0;  // parity bit of each stage of this warp's ring
+  const float kg = *a.k_g, vg = *a.v_g;
+
+  for (int64_t u = u0; u < u1;) {
+    // ---- the (sequence, tile, head) work that unit u belongs to
+    while (u >= base + units_of(span) * a.ix.hkv) {
+      base += units_of(span) * a.ix.hkv;
+      if (++tile * kRows >= (int64_t)seq.rows * a.group) {
+        tile = 0;
+        do seq = kv_sequence(a.ix, ++b, nullptr); while (seq.rows == 0);  // a later one has units: u < total
+      }
+      span = tile_span<kRows>(a, seq, tile);
+    }
+    const int64_t n = units_of(span);
+    const int head = (int)((u - base) / n);
+    const int64_t w0 = base + head * n;           // the work's first unit
+    const int j0 = (int)(u - w0);
+    const int j1 = (int)(u1 - w0 < n ? u1 - w0 : n);
+    u = w0 + j1;
+
+    // ---- queries: B fragments of Q^T, row r = tile*kRows + 8*nt + g of the head's rows
+    uint32_t qf[NT][2 * kSteps];
+    float factor[NT][2];        // score units of columns 2t, 2t+1
+    int32_t lo[NT][2], hi[NT][2];
+    int32_t all_lo = 0, all_hi = 0x7FFFFFFF;  // tokens that every row of the tile sees
+    const int64_t nrows = (int64_t)seq.rows * a.group;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int64_t r = tile * kRows + 8 * nt + g;
+      uint32_t raw[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) raw[i] = 0;
+      if (r < nrows) {
+        const int64_t tok = seq.row0 + r / a.group, hq = (int64_t)head * a.group + r % a.group;
+        const uint4* q4 = reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + hq * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 v = ld_stream(q4 + i);
+          raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+        }
+      }
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) mx = max(mx, mag_max_halves(raw[i]));
+      mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+      const int ex = query_exponent(__uint_as_float(mx << 16));
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {  // eight dimensions: pairs (0,4), (2,6), (1,5), (3,7) as codes_to_half
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[2 * e] = scale_exp2(__uint_as_float(raw[4 * w + e] << 16), ex);
+          f[2 * e + 1] = scale_exp2(__uint_as_float(raw[4 * w + e] & 0xFFFF0000u), ex);
+        }
+        qf[nt][4 * w] = half2_bits(f[0], f[4]);
+        qf[nt][4 * w + 1] = half2_bits(f[2], f[6]);
+        qf[nt][4 * w + 2] = half2_bits(f[1], f[5]);
+        qf[nt][4 * w + 3] = half2_bits(f[3], f[7]);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int64_t rc = tile * kRows + 8 * nt + 2 * t + c;
+        const int ec = __shfl_sync(0xFFFFFFFFu, ex, (2 * t + c) * 4);
+        factor[nt][c] = scale_exp2(a.scale * kg * 1.44269504f, 7 - ec);
+        Visible v{0, 0};
+        if (rc < nrows) v = visible((int64_t)seq.len - seq.rows + rc / a.group, seq.len, a.causal, a.window);
+        lo[nt][c] = v.lo;
+        hi[nt][c] = v.hi;
+        if (rc < nrows) {
+          all_lo = max(all_lo, v.lo);
+          all_hi = min(all_hi, v.hi);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      all_lo = max(all_lo, __shfl_xor_sync(0xFFFFFFFFu, all_lo, o));
+      all_hi = min(all_hi, __shfl_xor_sync(0xFFFFFFFFu, all_hi, o));
+    }
+
+    float m[NT][2], l[NT][2], o[NT][kSteps][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+    }
+
+    // ---- this warp's granules j0 + warp + 8*i of the work
+    const int cnt = span.n > 0 && j1 - j0 > warp ? (j1 - j0 - warp + kAttnWarps - 1) / kAttnWarps : 0;
+    const int gfirst = span.g0 + j0 + warp;
+    const int32_t* table = a.ix.table + (int64_t)b * a.ix.width;
+    int32_t ids = -1;  // lane i: page of granule (i0 & ~31) + i, -1 beyond the span or for a page that is none
+    auto fetch_ids = [&](int i0) {
+      const int i = i0 + lane;
+      int32_t p = -1;
+      if (i < cnt && NVFP4_IN_BOUNDS((gfirst + kAttnWarps * i) / gpp, a.ix.width, a.status)) {
+        p = table[(gfirst + kAttnWarps * i) / gpp];
+        if (p < 0 || p >= a.ix.num_pages) {
+          record_status(a.status, NVFP4_ERR_PAGE);
+          p = -1;
+        }
+      }
+      return p;
+    };
+    int32_t next_ids = -1;
+    auto issue = [&](int i) {  // called by the whole warp
+      if ((i & 31) == 0) next_ids = fetch_ids(i);
+      const int32_t p = __shfl_sync(0xFFFFFFFFu, next_ids, i & 31);
+      if (lane == 0 && p >= 0) {
+        const int gi = gfirst + kAttnWarps * i;
+        const int st = i % kStages;
+        int64_t at = (((int64_t)p * a.ix.hkv + head) * gpp + gi % gpp) * kGB;
+        if (!NVFP4_IN_BOUNDS(at + kGB - 1, a.ix.num_pages * a.ix.hkv * gpp * kGB, a.status)) at = 0;
+        const uint8_t* from = a.pages + at;
+        mbar_arrive_expect_tx(&sh.bar[warp][st], kGB);
+        bulk_load(sh.ring[warp][st], from, kGB, &sh.bar[warp][st]);
+      }
+    };
+    const int ahead = cnt < kStages - 1 ? cnt : kStages - 1;
+    for (int i = 0; i < ahead; ++i) issue(i);
+    int st = 0;
+    for (int i = 0; i < cnt; ++i) {
+      if (i + kStages - 1 < cnt) issue(i + kStages - 1);  // into the stage that the last iteration has read
+      if ((i & 31) == 0) ids = fetch_ids(i);
+      const int32_t page = __shfl_sync(0xFFFFFFFFu, ids, i & 31);
+      if (page < 0) {  // not a page: its tokens count as masked
+        if (++st == kStages) st = 0;
+        continue;
+      }
+      if (!sh.abort && !mbar_wait_warp(&sh.bar[warp][st], (phase >> st) & 1u, &sh.abort, kAttnWaitNs))
+        if (lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
+      phase ^= 1u << st;
+      const uint8_t* gr = sh.ring[warp][st];
+      if (++st == kStages) st = 0;
+
+      // S^T of 16 tokens
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+      {
+        uint32_t wa[kWords], wb[kWords];  // rows g and g + 8
+        const uint8_t* ka = gr + token_of(g) * (D / 2) + t * (D / 8);
+        const uint8_t* kb = gr + token_of(g + 8) * (D / 2) + t * (D / 8);
+        uint32_t sa, sb;  // scale bytes of the lane's D/4 dimensions (two blocks, or one)
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(ka), y = *reinterpret_cast<const uint4*>(kb);
+          wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w;
+          wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[3] = y.w;
+          sa = *reinterpret_cast<const uint16_t*>(gr + 8 * D + token_of(g) * 8 + 2 * t);
+          sb = *reinterpret_cast<const uint16_t*>(gr + 8 * D + token_of(g + 8) * 8 + 2 * t);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(ka), y = *reinterpret_cast<const uint2*>(kb);
+          wa[0] = x.x; wa[1] = x.y;
+          wb[0] = y.x; wb[1] = y.y;
+          sa = gr[8 * D + token_of(g) * 4 + t];
+          sb = gr[8 * D + token_of(g + 8) * 4 + t];
+        }
+#pragma unroll
+        for (int blk = 0; blk < D / 64; ++blk) {
+          const uint32_t fa = scales_to_half(__byte_perm(sa, 0, blk ? 0x4141 : 0x4040));
+          const uint32_t fb = scales_to_half(__byte_perm(sb, 0, blk ? 0x4141 : 0x4040));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int w = 2 * blk + h;
+            uint32_t pa[4], pb[4];
+            codes_to_half(wa[w], pa);
+            codes_to_half(wb[w], pb);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              pa[e] = hmul2(pa[e], fa);
+              pb[e] = hmul2(pb[e], fb);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_16816(s[nt], pa[0], pb[0], pa[1], pb[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
+              mma_16816(s[nt], pa[2], pb[2], pa[3], pb[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+            }
+          }
+        }
+      }
+
+      // scores in log2 units, mask, running maximum
+      const int tok0 = (gfirst + kAttnWarps * i) * kGranule;
+      const bool whole = tok0 >= all_lo && tok0 + kGranule <= all_hi;
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = e & 1;
+          s[nt][e] *= factor[nt][c];
+          if (!whole) {
+            const int tk = tok0 + token_of(g + (e & 2) * 4);
+            if (tk < lo[nt][c] || tk >= hi[nt][c]) s[nt][e] = -INFINITY;
+          }
+          grow |= s[nt][e] > m[nt][c] + kRescaleAt;
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(s[nt][c], s[nt][c + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+            const float m1 = fmaxf(m[nt][c], mx);
+            const float f = m[nt][c] == -INFINITY ? 0.0f : ex2(m[nt][c] - m1);
+            m[nt][c] = m1;
+            l[nt][c] *= f;
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+              o[nt][j][c] *= f;
+              o[nt][j][c + 2] *= f;
+            }
+          }
+      }
+      // P^T as B fragments: FP16 rounds p to 2^-11 of itself
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mm = m[nt][e & 1];
+          p[e] = ex2(s[nt][e] - (mm == -INFINITY ? 0.0f : mm));
+        }
+        l[nt][0] += p[0] + p[2];
+        l[nt][1] += p[1] + p[3];
+        pf[nt][0] = transpose_8x8(half2_bits(p[0], p[1]));
+        pf[nt][1] = transpose_8x8(half2_bits(p[2], p[3]));
+      }
+
+      // O^T += V^T P^T: m-tile j of a word holds dimensions 2j and 2j+1 of each lane's run
+      {
+        const uint8_t* v0 = gr + 9 * D;
+        const uint8_t* vs = gr + 17 * D;
+        constexpr int kVWords = D / 64;
+        uint32_t w[4][kVWords], f[2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tk = token_of(2 * t + (k & 1) + (k & 2) * 4);
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(v0 + tk * 64 + 8 * g);
+            w[k][0] = x.x;
+            w[k][1] = x.y;
+          } else {
+            w[k][0] = *reinterpret_cast<const uint32_t*>(v0 + tk * 32 + 4 * g);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int ta = token_of(2 * t + 8 * k), tb = token_of(2 * t + 1 + 8 * k);
+          const uint32_t x = D == 128 ? vs[ta * 8 + g] : vs[ta * 4 + (g >> 1)];
+          const uint32_t y = D == 128 ? vs[tb * 8 + g] : vs[tb * 4 + (g >> 1)];
+          f[k] = scales_to_half(x | (y << 16));
+        }
+#pragma unroll
+        for (int i2 = 0; i2 < 2 * kVWords; ++i2) {  // four dimensions of the lane's run at a time
+          uint32_t pa[4], pb[4];
+          const uint32_t sel = (i2 & 1) ? 0x7632 : 0x5410;
+          codes_to_half(__byte_perm(w[0][i2 >> 1], w[1][i2 >> 1], sel), pa);
+          codes_to_half(__byte_perm(w[2][i2 >> 1], w[3][i2 >> 1], sel), pb);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            pa[e] = hmul2(pa[e], f[0]);
+            pb[e] = hmul2(pb[e], f[1]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816(o[nt][2 * i2], pa[0], pa[2], pb[0], pb[2], pf[nt][0], pf[nt][1]);
+            mma_16816(o[nt][2 * i2 + 1], pa[1], pa[3], pb[1], pb[3], pf[nt][0], pf[nt][1]);
+          }
+        }
+      }
+      __syncwarp();  // the stage may be refilled
+    }
+
+    // ---- the warps' parts meet
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = l[nt][c];
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
+        if (g == 0) {
+          sh.wm[warp][8 * nt + 2 * t + c] = m[nt][c];
+          sh.wl[warp][8 * nt + 2 * t + c] = x;
+        }
+      }
+    __syncthreads();  // every warp has read its ring: the joining buffer may take its place
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int row = 8 * nt + 2 * t + c;
+        float mt = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) mt = fmaxf(mt, sh.wm[w][row]);
+        const float f = m[nt][c] == -INFINITY ? 0.0f : ex2(m[nt][c] - mt);
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j)  // dimensions 2j, 2j+1 of the run of D/8 that starts at g*D/8
+          *reinterpret_cast<float2*>(&sh.join[warp][row][g * (D / 8) + 2 * j]) =
+              make_float2(o[nt][j][c] * f, o[nt][j][c + 2] * f);
+      }
+    if (tid < kRows) {
+      float mt = -INFINITY, lt = 0.0f;
+      for (int w = 0; w < kAttnWarps; ++w) mt = fmaxf(mt, sh.wm[w][tid]);
+      for (int w = 0; w < kAttnWarps; ++w)
+        lt += sh.wm[w][tid] == -INFINITY ? 0.0f : sh.wl[w][tid] * ex2(sh.wm[w][tid] - mt);
+      sh.m[tid] = mt;
+      sh.l[tid] = lt;
+    }
+    __syncthreads();
+
+    // ---- a whole work is written out; a part goes to the workspace, and the last part joins them
+    const bool whole_work = j0 == 0 && j1 == n;
+    auto write_rows = [&](auto&& value) {  // value(row, d) = unnormalised sum; sh.m, sh.l as joined
+      for (int e = tid; e < kRows * (D / 2); e += kAttnThreads) {
+        const int row = e / (D / 2), d = (e % (D / 2)) * 2;
+        const int64_t r = tile * kRows + row;
+        if (r >= nrows) continue;
+        const int64_t tok = seq.row0 + r / a.group, hq = (int64_t)head * a.group + r % a.group;
+        const int64_t at = tok * a.ix.hkv * a.group + hq;
+        const float lt = sh.l[row];
+        const float f = lt == 0.0f ? 0.0f : 128.0f * vg / lt;  // no visible token: zeros
+        const float2 x = value(row, d);
+        if (!NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status)) continue;
+        *reinterpret_cast<uint32_t*>(a.out + at * D + d) = f32x2_to_bf16x2(x.x * f, x.y * f);
+        if (a.lse && d == 0) a.lse[at] = lt == 0.0f ? -INFINITY : (sh.m[row] + log2f(lt)) * 0.693147181f;
+      }
+    };
+    auto joined = [&](int row, int d) {
+      float2 x = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        const float2 y = *reinterpret_cast<const float2*>(&sh.join[w][row][d]);
+        x.x += y.x;
+        x.y += y.y;
+      }
+      return x;
+    };
+    constexpr int kPart = kRows * (D + 2);  // O, then m and l of each row
+    if (whole_work) {
+      write_rows(joined);
+    } else {
+      float* part = a.partial + (2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0)) * kPart;
+      for (int e = tid; e < kRows * (D / 2); e += kAttnThreads) {
+        const int row = e / (D / 2), d = (e % (D / 2)) * 2;
+        *reinterpret_cast<float2*>(part + row * D + d) = joined(row, d);
+      }
+      if (tid < kRows) {
+        part[kRows * D + tid] = sh.m[tid];
+        part[kRows * D + kRows + tid] = sh.l[tid];
+      }
+      __threadfence();
+      __syncthreads();
+      const int64_t c0 = w0 / per, c1 = (w0 + n - 1) / per;  // the CTAs that share the work
+      if (tid == 0) {
+        const int last = atomicAdd(&a.counters[c0], 1) == (int)(c1 - c0);
+        if (last) a.counters[c0] = 0;  // ready for the next call
+        __threadfence();
+        sh.last = last;
+      }
+      __syncthreads();
+      if (sh.last) {
+        auto part_of = [&](int64_t c) { return a.partial + (2 * c + (c == c0 ? 1 : 0)) * kPart; };
+        if (tid < kRows) {
+          float mt = -INFINITY, lt = 0.0f;
+          for (int64_t c = c0; c <= c1; ++c) mt = fmaxf(mt, __ldcg(part_of(c) + kRows * D + tid));
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float mc = __ldcg(part_of(c) + kRows * D + tid);
+            lt += mc == -INFINITY ? 0.0f : __ldcg(part_of(c) + kRows * D + kRows + tid) * ex2(mc - mt);
+          }
+          sh.m[tid] = mt;
+          sh.l[tid] = lt;
+        }
+        __syncthreads();
+        write_rows([&](int row, int d) {
+          float2 x = make_float2(0.0f, 0.0f);
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float* p = part_of(c);
+            const float mc = __ldcg(p + kRows * D + row);
+            const float f = mc == -INFINITY ? 0.0f : ex2(mc - sh.m[row]);
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(p + row * D + d));
+            x.x += y.x * f;
+            x.y += y.y * f;
+          }
+          return x;
+        });
+      }
+    }
+    fence_proxy_async_smem();  // the joining buffer's place is filled by bulk copies again
+    __syncthreads();
+  }
+}
+
+constexpr int kMaxAttnCtas = 512;
+constexpr int kPartFloats = 16 * (128 + 2);
+
+size_t kv_attention_workspace_bytes() {
+  return (size_t)kMaxAttnCtas * sizeof(int32_t) + (size_t)2 * kMaxAttnCtas * kPartFloats * sizeof(float);
+}
+
+template <int D, int NT>
+cudaError_t launch_rows(AttnArgs a, int num_sms, cudaStream_t s) {
+  using Sh = AttnShared<D, NT>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kv_attention_kernel<D, NT>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Sh));
+  if (attr != cudaSuccess) return attr;
+  const int64_t want = (NT == 1 ? 2 : 1) * (int64_t)num_sms;
+  const int grid = (int)(want < kMaxAttnCtas ? want : kMaxAttnCtas);
+  note_launch();
+  kv_attention_kernel<D, NT><<<grid, kAttnThreads, sizeof(Sh), s>>>(a, 2 * kAttnWarps);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_attention(AttnArgs a, int D, int64_t max_q, void* workspace, int num_sms, cudaStream_t s) {
+  if (a.ix.total == 0 || a.ix.batch == 0) return cudaSuccess;
+  a.counters = static_cast<int32_t*>(workspace);
+  a.partial = reinterpret_cast<float*>(a.counters + kMaxAttnCtas);
+  const bool one = max_q * a.group <= 8;
+  if (D == 128) return one ? launch_rows<128, 1>(a, num_sms, s) : launch_rows<128, 2>(a, num_sms, s);
+  return one ? launch_rows<64, 1>(a, num_sms, s) : launch_rows<64, 2>(a, num_sms, s);
+}
+
+}  // namespace nvfp4
