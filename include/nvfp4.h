@@ -368,9 +368,10 @@ nvfp4_status nvfp4_kv_append(const void* k, const void* v, int64_t row_stride, i
                              int64_t num_pages, int page_size, const float* k_g, const float* v_g,
                              nvfp4_mode mode, nvfp4_stream_t stream);
 
-/* Workspace bytes of nvfp4_paged_attention. Zero-fill it once before its first
- * use; every call leaves it ready for the next. Calls that share one must be
- * ordered on the GPU. Host only. */
+/* Workspace bytes of nvfp4_paged_attention. Zero-fill its first 2048 bytes once
+ * before the first use; every call leaves them ready for the next (zero-fill
+ * them again after a call that reported NVFP4_ERR_TIMEOUT). Calls that share a
+ * workspace must be ordered on the GPU. Host only. */
 size_t nvfp4_paged_attention_workspace_bytes(void);
 
 /*

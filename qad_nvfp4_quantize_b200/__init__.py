@@ -183,7 +183,7 @@ def _reset_workspaces(device_index: int) -> None:
     """Zero-fill every cached workspace of one device (after a timed-out wait).
     Each is cleared on the stream that uses it, after the work queued there."""
     with _ws_lock:
-        items = [entry for key, entry in _ws_cache.items() if key[0] == device_index]
+        items = [entry for cache in (_ws_cache, _attn_ws) for key, entry in cache.items() if key[0] == device_index]
     for stream, ws in items:
         with torch.cuda.stream(stream):
             ws.zero_()
@@ -453,23 +453,27 @@ def _kv_cache_of(cache: KVCache):
     return dev, pages.shape[0], pages.shape[1]
 
 
-# The attention's workspace holds counters that are zero between calls. One per
-# (device, stream) outside of graph capture; a captured call takes one of its
-# own from the graph's memory, zeroed by the graph, so that graphs replayed at
-# the same time, and eager calls beside them, share nothing.
+# The attention's workspace begins with counters that are zero between calls.
+# One per (device, stream) outside of graph capture; a captured call takes one
+# of its own from the graph's memory, whose counters the graph zeroes, so that
+# graphs replayed at the same time, and eager calls beside them, share nothing.
+_ATTN_COUNTERS = 2048
 _attn_ws: dict = {}
 
 
 def _attention_workspace(dev: torch.device) -> torch.Tensor:
-    nbytes = int(lib().nvfp4_paged_attention_workspace_bytes())
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        ws = torch.empty(int(lib().nvfp4_paged_attention_workspace_bytes()), dtype=torch.uint8, device=dev)
+        ws[:_ATTN_COUNTERS].zero_()
+        return ws
     stream = torch.cuda.current_stream(dev)
     key = (dev.index, stream.cuda_stream)
-    with _ws_lock:
-        entry = _attn_ws.get(key)
-        if entry is None:
-            entry = _attn_ws[key] = (stream, torch.zeros(nbytes, dtype=torch.uint8, device=dev))
+    entry = _attn_ws.get(key)
+    if entry is None:
+        ws = torch.empty(int(lib().nvfp4_paged_attention_workspace_bytes()), dtype=torch.uint8, device=dev)
+        ws[:_ATTN_COUNTERS].zero_()
+        with _ws_lock:
+            entry = _attn_ws.setdefault(key, (stream, ws))
     return entry[1]
 
 

@@ -318,7 +318,7 @@ nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_stride, int64_t tota
   if (!kv_shape_ok(page_size, head_dim) || !kv_sizes_ok(total, kv_heads, batch, table_width, num_pages, page_size))
     return NVFP4_ERR_INVALID_ARG;
   if (q_heads <= 0 || q_heads % kv_heads || q_heads / kv_heads > 128) return NVFP4_ERR_INVALID_ARG;
-  if (total * (q_heads / kv_heads) >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+  if (total * (q_heads / kv_heads) >= (int64_t(1) << 30)) return NVFP4_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || scale > 3.0e38f || window < 0 || max_q < 0) return NVFP4_ERR_INVALID_ARG;
   if (q_stride % 8 || q_stride < (int64_t)q_heads * head_dim) return NVFP4_ERR_INVALID_ARG;
   if (total > 0 && batch > 0) {

@@ -96,7 +96,9 @@ struct AttnArgs;
 cudaError_t launch_kv_append(const void* k, const void* v, int64_t stride, int D, const KvIndex& ix, uint8_t* pages,
                              const float* k_g, const float* v_g, bool fos, int* status, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_attention(AttnArgs a, int D, int64_t max_q, void* workspace, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_prefill(const AttnArgs& a, int D, int num_sms, cudaStream_t s);
 size_t kv_attention_workspace_bytes();
+size_t kv_prefill_partial_floats();
 struct PoolArgs {
   int32_t* refs;
   int32_t* table;

@@ -21,13 +21,11 @@
 //
 // Every warp works alone: granule i of a CTA's span goes to warp i mod 8, which
 // keeps kStages bulk copies of 18*D bytes in flight on its own barriers and its
-// own m, l, O; the warps meet at the end of the span. The spans come from
-// cutting the list of all granules of all (sequence, row tile, head) works into
-// equal parts, one per CTA, on the device, from the lengths as they are at run
-// time: ragged batches and graphs replayed with other lengths stay balanced. A
-// work cut by such a boundary leaves partial (m, l, O) in the workspace; the
-// last CTA that arrives at the work's counter joins the parts in index order
-// (no CTA waits, and the result does not depend on which one is last).
+// own m, l, O; the warps meet at the end of the span. A work that the cut of the
+// work list (kv_attention.cuh) divides leaves partial (m, l, O) in the
+// workspace; the last CTA that arrives at the work's counter joins the parts in
+// index order (no CTA waits, and the result does not depend on which one is
+// last).
 #include <cuda_fp16.h>
 
 #include "kv_attention.cuh"
@@ -36,7 +34,6 @@ namespace nvfp4 {
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr uint64_t kAttnWaitNs = 2000000000ull;
 constexpr float kRescaleAt = 8.0f;
 
 template <int D, int NT>
@@ -47,13 +44,12 @@ struct AttnShared {
   union {
     uint8_t ring[kAttnWarps][kStages][granule_bytes(D)];
     float join[kAttnWarps][kRows][kPad];
+    PartShared part;
   };
   uint64_t bar[kAttnWarps][kStages];
   float wm[kAttnWarps][kRows], wl[kAttnWarps][kRows];
   float m[kRows], l[kRows];
-  int64_t scan[kAttnWarps + 1];
-  int64_t found_base;
-  int found_b, last, abort;
+  int last, abort;
 };
 
 NVFP4_DEVINL void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -79,58 +75,6 @@ __host__ __device__ constexpr int token_of(int i) {
   return (i & 8) + ((i & 1) ? (((i & 7) >> 1) + 4) ^ 1 : (i & 7) >> 1);
 }
 
-// The granules that a row tile of a sequence needs: first granule and count
-// (0 when no row of the tile sees a token).
-struct Span {
-  int32_t g0, n;
-};
-template <int kRows>
-NVFP4_DEVINL Span tile_span(const AttnArgs& a, const KvSeq& s, int64_t tile) {
-  const int64_t r1 = (tile + 1) * kRows < (int64_t)s.rows * a.group ? (tile + 1) * kRows : (int64_t)s.rows * a.group;
-  const int64_t first = tile * kRows / a.group, last = (r1 - 1) / a.group, pos = (int64_t)s.len - s.rows;
-  const Visible v0 = visible(pos + first, s.len, a.causal, a.window);
-  const Visible v1 = visible(pos + last, s.len, a.causal, a.window);
-  if (v1.hi <= v0.lo) return Span{0, 0};
-  const int32_t g0 = v0.lo / kGranule;
-  return Span{g0, (v1.hi + kGranule - 1) / kGranule - g0};
-}
-// Work units of a tile for one head: its granules, at least one (an empty tile
-// still writes its rows).
-NVFP4_DEVINL int64_t units_of(const Span& s) { return s.n > 0 ? s.n : 1; }
-
-template <int kRows>
-NVFP4_DEVINL int64_t sequence_units(const AttnArgs& a, int b, int* status) {
-  const KvSeq s = kv_sequence(a.ix, b, status);
-  const int64_t tiles = ((int64_t)s.rows * a.group + kRows - 1) / kRows;
-  int64_t u = 0;
-  for (int64_t t = 0; t < tiles; ++t) u += units_of(tile_span<kRows>(a, s, t));
-  return u * a.ix.hkv;
-}
-
-// Exclusive scan over the CTA; total in *total.
-template <class Sh>
-NVFP4_DEVINL int64_t cta_scan(Sh& sh, int64_t v, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += u;
-  }
-  __syncthreads();
-  if (lane == 31) sh.scan[warp] = incl;
-  __syncthreads();
-  int64_t pre = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kAttnWarps; ++w) {
-    const int64_t x = sh.scan[w];
-    pre += w < warp ? x : 0;
-    all += x;
-  }
-  *total = all;
-  return pre + incl - v;
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_kernel(const AttnArgs a, int min_units) {
   using Sh = AttnShared<D, NT>;
@@ -147,53 +91,29 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
   if (tid == 0) sh.abort = 0;
   fence_barrier_init();
 
-  // ---- this CTA's span of the list of all units
-  int64_t total = 0;
-  {
-    int64_t mine = 0;
-    for (int b = tid; b < a.ix.batch; b += kAttnThreads) mine += sequence_units<kRows>(a, b, a.status);
-    cta_scan(sh, mine, &total);
-  }
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < min_units) per = min_units;
-  const int64_t u0 = per * blockIdx.x, u1 = u0 + per < total ? u0 + per : total;
+  // ---- this CTA's part of the list of units
+  int64_t per = 0;
+  auto first_unit = [&](int64_t total) {
+    per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < min_units) per = min_units;
+    return per * blockIdx.x;
+  };
+  find_part<kRows, 1, kAttnThreads>(a, sh.part, first_unit);
+  const int64_t total = sh.part.total, u0 = first_unit(total), u1 = u0 + per < total ? u0 + per : total;
   if (u0 >= u1) return;
-  for (int64_t base = 0, b0 = 0;; b0 += kAttnThreads) {
-    const int b = (int)b0 + tid;
-    const int64_t v = b < a.ix.batch ? sequence_units<kRows>(a, b, nullptr) : 0;
-    int64_t sum;
-    const int64_t pre = base + cta_scan(sh, v, &sum);
-    if (u0 >= pre && u0 < pre + v) {
-      sh.found_b = b;
-      sh.found_base = pre;
-    }
-    base += sum;
-    if (u0 < base) break;
-  }
-  __syncthreads();
-  int b = sh.found_b;
-  int64_t base = sh.found_base, tile = 0;
-  KvSeq seq = kv_sequence(a.ix, b, nullptr);
-  Span span = tile_span<kRows>(a, seq, 0);
+  WorkCursor<kRows, 1> w;
+  w.start(a, sh.part.b, sh.part.tile, sh.part.base, u0);
+  fence_proxy_async_smem();
+  __syncthreads();  // the search's scratch lies over the ring
   uint32_t phase = 0;  // parity bit of each stage of this warp's ring
   const float kg = *a.k_g, vg = *a.v_g;
 
-  for (int64_t u = u0; u < u1;) {
-    // ---- the (sequence, tile, head) work that unit u belongs to
-    while (u >= base + units_of(span) * a.ix.hkv) {
-      base += units_of(span) * a.ix.hkv;
-      if (++tile * kRows >= (int64_t)seq.rows * a.group) {
-        tile = 0;
-        do seq = kv_sequence(a.ix, ++b, nullptr); while (seq.rows == 0);  // a later one has units: u < total
-      }
-      span = tile_span<kRows>(a, seq, tile);
-    }
-    const int64_t n = units_of(span);
-    const int head = (int)((u - base) / n);
-    const int64_t w0 = base + head * n;           // the work's first unit
-    const int j0 = (int)(u - w0);
-    const int j1 = (int)(u1 - w0 < n ? u1 - w0 : n);
-    u = w0 + j1;
+  for (int64_t u = u0;;) {
+    const int j0 = (int)(u - w.w0);
+    const int j1 = (int)(u1 - w.w0 < w.n ? u1 - w.w0 : w.n);
+    u = w.w0 + j1;
+    const KvSeq& seq = w.seq;
+    const int tile = w.tile, head = w.head, n = w.n, b = w.b;
 
     // ---- queries: B fragments of Q^T, row r = tile*kRows + 8*nt + g of the head's rows
     uint32_t qf[NT][2 * kSteps];
@@ -203,7 +123,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     const int64_t nrows = (int64_t)seq.rows * a.group;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int64_t r = tile * kRows + 8 * nt + g;
+      const int64_t r = (int64_t)tile * kRows + 8 * nt + g;
       uint32_t raw[D / 8];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) raw[i] = 0;
@@ -237,9 +157,9 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int64_t rc = tile * kRows + 8 * nt + 2 * t + c;
+        const int64_t rc = (int64_t)tile * kRows + 8 * nt + 2 * t + c;
         const int ec = __shfl_sync(0xFFFFFFFFu, ex, (2 * t + c) * 4);
-        factor[nt][c] = scale_exp2(a.scale * kg * 1.44269504f, 7 - ec);
+        factor[nt][c] = scale_exp2(a.scale * kg * kLog2e, 7 - ec);
         Visible v{0, 0};
         if (rc < nrows) v = visible((int64_t)seq.len - seq.rows + rc / a.group, seq.len, a.causal, a.window);
         lo[nt][c] = v.lo;
@@ -266,8 +186,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     }
 
     // ---- this warp's granules j0 + warp + 8*i of the work
-    const int cnt = span.n > 0 && j1 - j0 > warp ? (j1 - j0 - warp + kAttnWarps - 1) / kAttnWarps : 0;
-    const int gfirst = span.g0 + j0 + warp;
+    const int cnt = w.span.n > 0 && j1 - j0 > warp ? (j1 - j0 - warp + kAttnWarps - 1) / kAttnWarps : 0;
+    const int gfirst = w.span.g0 + j0 + warp;
     const int32_t* table = a.ix.table + (int64_t)b * a.ix.width;
     int32_t ids = -1;  // lane i: page of granule (i0 & ~31) + i, -1 beyond the span or for a page that is none
     auto fetch_ids = [&](int i0) {
@@ -501,7 +421,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     auto write_rows = [&](auto&& value) {  // value(row, d) = unnormalised sum; sh.m, sh.l as joined
       for (int e = tid; e < kRows * (D / 2); e += kAttnThreads) {
         const int row = e / (D / 2), d = (e % (D / 2)) * 2;
-        const int64_t r = tile * kRows + row;
+        const int64_t r = (int64_t)tile * kRows + row;
         if (r >= nrows) continue;
         const int64_t tok = seq.row0 + r / a.group, hq = (int64_t)head * a.group + r % a.group;
         const int64_t at = tok * a.ix.hkv * a.group + hq;
@@ -510,7 +430,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
         const float2 x = value(row, d);
         if (!NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status)) continue;
         *reinterpret_cast<uint32_t*>(a.out + at * D + d) = f32x2_to_bf16x2(x.x * f, x.y * f);
-        if (a.lse && d == 0) a.lse[at] = lt == 0.0f ? -INFINITY : (sh.m[row] + log2f(lt)) * 0.693147181f;
+        if (a.lse && d == 0) a.lse[at] = lt == 0.0f ? -INFINITY : (sh.m[row] + log2f(lt)) * kLn2;
       }
     };
     auto joined = [&](int row, int d) {
@@ -538,7 +458,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       }
       __threadfence();
       __syncthreads();
-      const int64_t c0 = w0 / per, c1 = (w0 + n - 1) / per;  // the CTAs that share the work
+      const int64_t c0 = w.w0 / per, c1 = (w.w0 + n - 1) / per;  // the CTAs that share the work
       if (tid == 0) {
         const int last = atomicAdd(&a.counters[c0], 1) == (int)(c1 - c0);
         if (last) a.counters[c0] = 0;  // ready for the next call
@@ -575,14 +495,17 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     }
     fence_proxy_async_smem();  // the joining buffer's place is filled by bulk copies again
     __syncthreads();
+    if (u >= u1 || !w.next(a)) break;
   }
 }
 
 constexpr int kMaxAttnCtas = 512;
+constexpr int kCounters = 512;
 constexpr int kPartFloats = 16 * (128 + 2);
 
 size_t kv_attention_workspace_bytes() {
-  return (size_t)kMaxAttnCtas * sizeof(int32_t) + (size_t)2 * kMaxAttnCtas * kPartFloats * sizeof(float);
+  const size_t rows = (size_t)2 * kMaxAttnCtas * kPartFloats, tiles = kv_prefill_partial_floats();
+  return kCounters * sizeof(int32_t) + (rows > tiles ? rows : tiles) * sizeof(float);
 }
 
 template <int D, int NT>
@@ -601,7 +524,8 @@ cudaError_t launch_rows(AttnArgs a, int num_sms, cudaStream_t s) {
 cudaError_t launch_kv_attention(AttnArgs a, int D, int64_t max_q, void* workspace, int num_sms, cudaStream_t s) {
   if (a.ix.total == 0 || a.ix.batch == 0) return cudaSuccess;
   a.counters = static_cast<int32_t*>(workspace);
-  a.partial = reinterpret_cast<float*>(a.counters + kMaxAttnCtas);
+  a.partial = reinterpret_cast<float*>(a.counters + kCounters);
+  if (max_q == 0 || max_q * a.group > 16) return launch_kv_prefill(a, D, num_sms, s);
   const bool one = max_q * a.group <= 8;
   if (D == 128) return one ? launch_rows<128, 1>(a, num_sms, s) : launch_rows<128, 2>(a, num_sms, s);
   return one ? launch_rows<64, 1>(a, num_sms, s) : launch_rows<64, 2>(a, num_sms, s);

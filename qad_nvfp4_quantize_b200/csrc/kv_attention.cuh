@@ -90,4 +90,177 @@ struct AttnArgs {
   int* status;
 };
 
+
+constexpr uint64_t kAttnWaitNs = 2000000000ull;  // bound of every wait
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
+// ---------------------------------------------------------------------------
+// Work list. A work is one KV head of one tile of kRows query rows of one
+// sequence (row r = new token r / group, query head r % group of the KV head);
+// its units are runs of kUnit granules that some row of the tile sees, at least
+// one (a tile that sees nothing still writes its rows). The works of a launch
+// in order (sequence, tile, head) and their units form one list, from which
+// every CTA takes an equal part: the lengths are read on the device, so ragged
+// batches, and graphs replayed with other lengths, stay balanced.
+// ---------------------------------------------------------------------------
+struct Span {
+  int32_t g0, n;  // first granule, number of granules
+};
+template <int kRows>
+NVFP4_DEVINL Span tile_span(const AttnArgs& a, const KvSeq& s, int tile) {
+  const int32_t rows = s.rows * a.group;
+  const int32_t r1 = rows - tile * kRows < kRows ? rows : (tile + 1) * kRows;
+  const int32_t first = tile * kRows / a.group, last = (r1 - 1) / a.group, pos = s.len - s.rows;
+  const Visible v0 = visible((int64_t)pos + first, s.len, a.causal, a.window);
+  const Visible v1 = visible((int64_t)pos + last, s.len, a.causal, a.window);
+  if (v1.hi <= v0.lo) return Span{0, 0};
+  const int32_t g0 = v0.lo / kGranule;
+  return Span{g0, (v1.hi + kGranule - 1) / kGranule - g0};
+}
+template <int kRows>
+NVFP4_DEVINL int tiles_of(const AttnArgs& a, const KvSeq& s) {
+  return (s.rows * a.group + (kRows - 1)) / kRows;
+}
+template <int kUnit>
+NVFP4_DEVINL int units_of(const Span& s) {
+  return s.n > 0 ? (s.n + kUnit - 1) / kUnit : 1;
+}
+
+constexpr int kStoredSums = 512, kLongList = 64, kLongTiles = 16;
+
+// Scratch of find_part (may lie over buffers that are not in use yet).
+struct PartShared {
+  int64_t sums[kStoredSums];
+  int64_t warp_total[32];
+  int32_t long_seq[kLongList];
+  int32_t long_count;
+  int64_t total, base;
+  int32_t b, tile;
+};
+
+// The units in all, and the (sequence, tile) that unit `u0(total)` lies in with
+// the index of that tile's first unit. Called by all kThreads threads; a thread
+// counts a sequence, a warp one of many tiles.
+template <int kRows, int kUnit, int kThreads, class First>
+NVFP4_DEVINL void find_part(const AttnArgs& a, PartShared& sh, First first) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto count = [&](const KvSeq& s, int t0, int step) {
+    int64_t u = 0;
+    const int tiles = tiles_of<kRows>(a, s);
+    for (int t = t0; t < tiles; t += step) u += units_of<kUnit>(tile_span<kRows>(a, s, t));
+    return u * a.ix.hkv;
+  };
+  if (tid == 0) sh.long_count = 0;
+  __syncthreads();
+  int64_t mine = 0;
+  for (int b = tid; b < a.ix.batch; b += kThreads) {
+    const KvSeq s = kv_sequence(a.ix, b, a.status);
+    if (tiles_of<kRows>(a, s) > kLongTiles && b < kStoredSums) {
+      const int i = atomicAdd(&sh.long_count, 1);
+      if (i < kLongList) {
+        sh.long_seq[i] = b;
+        continue;
+      }
+    }
+    const int64_t u = count(s, 0, 1);
+    if (b < kStoredSums) sh.sums[b] = u;
+    mine += u;
+  }
+  __syncthreads();
+  const int longs = sh.long_count < kLongList ? sh.long_count : kLongList;
+  for (int i = warp; i < longs; i += kThreads / 32) {
+    const int b = sh.long_seq[i];
+    int64_t u = count(kv_sequence(a.ix, b, nullptr), lane, 32);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+    if (lane == 0) {
+      sh.sums[b] = u;
+      mine += u;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+  if (lane == 0) sh.warp_total[warp] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t total = lane < kThreads / 32 ? sh.warp_total[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    const int64_t u0 = first(total);
+    // inclusive scan of 32 values; the lane whose part of the list holds u0
+    int64_t base = 0;
+    auto locate = [&](int64_t v) {
+      int64_t incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const unsigned at = __ballot_sync(0xFFFFFFFFu, base + incl > u0);
+      const int src = at ? __ffs(at) - 1 : 31;
+      base += __shfl_sync(0xFFFFFFFFu, at ? incl - v : incl, src);
+      return at ? src : -1;
+    };
+    if (u0 < total) {
+      int b = -1, tile = -1;
+      for (int b0 = 0; b < 0 && b0 < a.ix.batch; b0 += 32) {
+        const int x = b0 + lane;
+        int64_t v = 0;
+        if (x < a.ix.batch) v = x < kStoredSums ? sh.sums[x] : count(kv_sequence(a.ix, x, nullptr), 0, 1);
+        const int src = locate(v);
+        if (src >= 0) b = b0 + src;
+      }
+      const KvSeq s = b < 0 ? KvSeq{0, 0, 0} : kv_sequence(a.ix, b, nullptr);
+      const int tiles = tiles_of<kRows>(a, s);
+      for (int t0 = 0; tile < 0 && t0 < tiles; t0 += 32) {
+        const int x = t0 + lane;
+        const int src = locate(x < tiles ? (int64_t)units_of<kUnit>(tile_span<kRows>(a, s, x)) * a.ix.hkv : 0);
+        if (src >= 0) tile = t0 + src;
+      }
+      if (tile < 0) total = 0;  // lengths that another stream changes meanwhile: no work rather than a wrong one
+      if (lane == 0) {
+        sh.b = b;
+        sh.tile = tile;
+        sh.base = base;
+      }
+    }
+    if (lane == 0) sh.total = total;
+  }
+  __syncthreads();
+}
+
+// A CTA's place in the list, moved from work to work. Every thread keeps its
+// own copy (the values are the same in all of them).
+template <int kRows, int kUnit>
+struct WorkCursor {
+  KvSeq seq;
+  Span span;
+  int b, tile, head, n;  // n: units of the work
+  int64_t w0;            // the work's first unit
+  NVFP4_DEVINL void start(const AttnArgs& a, int b_, int tile_, int64_t tile_base, int64_t u) {
+    b = b_;
+    tile = tile_;
+    seq = kv_sequence(a.ix, b, nullptr);
+    span = tile_span<kRows>(a, seq, tile);
+    n = units_of<kUnit>(span);
+    head = (int)((u - tile_base) / n);
+    w0 = tile_base + (int64_t)head * n;
+  }
+  NVFP4_DEVINL bool next(const AttnArgs& a) {  // false behind the last work
+    w0 += n;
+    if (++head < a.ix.hkv) return true;
+    head = 0;
+    if (++tile >= tiles_of<kRows>(a, seq)) {
+      tile = 0;
+      do {
+        if (++b >= a.ix.batch) return false;
+        seq = kv_sequence(a.ix, b, nullptr);
+      } while (seq.rows == 0);
+    }
+    span = tile_span<kRows>(a, seq, tile);
+    n = units_of<kUnit>(span);
+    return true;
+  }
+};
+
 }  // namespace nvfp4

@@ -1,0 +1,626 @@
+// nvfp4_paged_attention for many query rows per KV head (prompts, chunks):
+// the same mathematics as kv_attention.cu on tcgen05 tensor cores.
+//
+// Bound: the tensor pipe (4*D FLOP per row and token), the 2^x unit (16 a cycle
+// and SM: as long as the two MMAs of a 128 x 128 tile with D = 128) and the
+// issue slots that dequantization and softmax share.
+//
+// One CTA per SM walks its part of the work list; a work is 256 query rows (two
+// tiles of 128) of one KV head against its cached tokens, 128 at a time.
+//   warps 0..3, 4..7   softmax of row tile 0 and 1, a thread per row: scores
+//                      from tensor memory, p = 2^(s*c - m) as FP16 pairs back
+//                      into the same columns, the output's rescaling and the
+//                      epilogue;
+//   warps 8..11        dequantization: each keeps bulk copies of its granules
+//                      in flight (ring of kRing) and writes K and V as FP16
+//                      rows of 64 dimensions, 128-byte swizzled, two stages;
+//   warps 12, 13       issue the MMAs of row tile 0 and 1: S = Q K^T (K-major
+//                      operands), O += P V (P from tensor memory, V read with
+//                      its 64-dimension runs as the MN-major operand).
+// Two row tiles take turns: while one is in softmax the tensor pipe works for
+// the other, and each dequantized tile serves 256 rows. Tensor memory: S/P 128
+// columns and O D columns per row tile. S of the next tile is issued once P V
+// of this one is complete (its columns hold P), which also means that O is at
+// rest whenever a softmax warp has scores to look at: it rescales O by itself.
+//
+// The running maximum m is allowed to lag: a row keeps m while the sum of its
+// tile's p stays below 2^14 (then every p fits FP16) and takes the true maximum
+// otherwise, so the usual tile needs no maximum at all.
+//
+// Head dimensions are stored in the order in which codes_to_half yields them
+// (0,4,2,6,1,5,3,7 of each eight), in Q as in K; the epilogue restores V's.
+#include <cuda_fp16.h>
+
+#include "kv_attention.cuh"
+
+namespace nvfp4 {
+
+constexpr int kPreThreads = 512;
+constexpr int kPreRows = 256;
+constexpr int kTileTokens = 128;
+constexpr int kUnitGranules = kTileTokens / kGranule;
+constexpr float kStartMax = -1e30f;  // m before the first visible token, in log2 units
+constexpr float kSumLimit = 16384.0f;
+
+template <int D>
+struct PreShared {
+  static constexpr int kRing = 3;
+  static constexpr int kTile = kTileTokens * D * 2;  // bytes of an FP16 tile
+  uint8_t k[2][kTile];
+  uint8_t v[2][kTile];
+  union {
+    uint8_t q[2][kTile];
+    PartShared part;
+  };
+  uint8_t ring[4][kRing][granule_bytes(D)];
+  uint64_t ring_full[4][kRing];
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2], group[2];
+  uint32_t tmem;
+  int last[2];
+  volatile int abort;
+};
+
+// kind::f16 instruction descriptor: D FP32, A and B FP16, M = 128.
+__host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+NVFP4_DEVINL void mma_f16_ss_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(NVFP4_ELECT_BEGIN ".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;" NVFP4_ELECT_END
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+NVFP4_DEVINL void mma_f16_ts_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(NVFP4_ELECT_BEGIN ".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;" NVFP4_ELECT_END
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// 32 columns of this warp's 32 tensor-memory lanes, with the wait: one statement, so that the compiler moves or spills
+// no register of a load that is still under way.
+NVFP4_DEVINL void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+NVFP4_DEVINL void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+NVFP4_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+template <int kRegs>
+NVFP4_DEVINL void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+NVFP4_DEVINL void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+NVFP4_DEVINL f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+NVFP4_DEVINL f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+NVFP4_DEVINL uint32_t half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Byte of 16-byte chunk c (0..7) of row r of half h (64 dimensions) in a 128-byte-swizzled tile.
+NVFP4_DEVINL uint32_t tile_chunk(int h, int r, int c) {
+  return (uint32_t)(h * kTileTokens * 128 + r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnArgs a) {
+  using Sh = PreShared<D>;
+  constexpr int kGB = granule_bytes(D), kRing = Sh::kRing, kSteps = D / 16;
+  extern __shared__ uint8_t pre_smem[];
+  Sh& sh = *reinterpret_cast<Sh*>((reinterpret_cast<uintptr_t>(pre_smem) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gpp = a.ix.page / kGranule;
+
+  if (tid == 0) {
+    for (int w = 0; w < 4; ++w)
+      for (int i = 0; i < kRing; ++i) mbar_init(&sh.ring_full[w][i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 4);
+      mbar_init(&sh.k_full[i], 4);
+      mbar_init(&sh.v_full[i], 4);
+      mbar_init(&sh.k_empty[i], 2);
+      mbar_init(&sh.v_empty[i], 2);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.group[i], 4);
+    }
+    sh.abort = 0;
+    fence_barrier_init();
+  }
+  int64_t per = 0;
+  auto first_unit = [&](int64_t total) {
+    per = (total + gridDim.x - 1) / gridDim.x;
+    return per * blockIdx.x;
+  };
+  find_part<kPreRows, kUnitGranules, kPreThreads>(a, sh.part, first_unit);
+  const int64_t total = sh.part.total, u0 = first_unit(total), u1 = u0 + per < total ? u0 + per : total;
+  if (u0 >= u1) return;
+  WorkCursor<kPreRows, kUnitGranules> w;
+  w.start(a, sh.part.b, sh.part.tile, sh.part.base, u0);
+  fence_proxy_async_smem();
+  if (warp == 12) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();  // the search's scratch lies over Q
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  auto timed_out = [&]() {
+    if (lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, &sh.abort, kAttnWaitNs); };
+  // unit range of this CTA within the work
+  auto from_unit = [&](int64_t u) { return (int)(u - w.w0); };
+  auto to_unit = [&]() { return (int)(u1 - w.w0 < w.n ? u1 - w.w0 : (int64_t)w.n); };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------- softmax
+    regs_inc<168>();  // 2 * 168 + 104 + 72 = 4 * 128, what the block was launched with
+    const int i = warp >> 2, wq = warp & 3, row = tid & 127;
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + i * 128, t_o = tmem + lane_base + 256 + i * D;
+    const float kg = *a.k_g, vg = *a.v_g;
+    uint32_t tiles = 0;  // tiles done by this row tile
+    uint32_t meets = 0;
+    auto meet = [&]() {  // the four warps of the row tile, with the usual bound
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.group[i]);
+      return wait(&sh.group[i], meets++ & 1);
+    };
+    bool ok = true;
+    for (int64_t u = u0; ok;) {
+      const int j0 = from_unit(u), j1 = to_unit();
+      u = w.w0 + j1;
+      const int32_t nrows = w.seq.rows * a.group;
+      const int32_t r0 = w.tile * kPreRows + i * 128, r = r0 + row;
+      if (r0 < nrows) {
+        // ---- this thread's query row as FP16, its power of two taken out
+        const bool live = r < nrows;
+        const int64_t tok = w.seq.row0 + r / a.group, hq = (int64_t)w.head * a.group + r % a.group;
+        const uint4* q4 = reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + hq * D);
+        uint32_t mx = 0;
+        if (live)
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = ld_stream(q4 + c);
+            mx = max(max(mx, mag_max_halves(x.x)), max(mag_max_halves(x.y), max(mag_max_halves(x.z), mag_max_halves(x.w))));
+          }
+        const int ex = query_exponent(__uint_as_float(mx << 16));
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (live) x = ld_stream(q4 + c);
+          float f[8];
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[2 * e] = scale_exp2(__uint_as_float(xs[e] << 16), ex);
+            f[2 * e + 1] = scale_exp2(__uint_as_float(xs[e] & 0xFFFF0000u), ex);
+          }
+          *reinterpret_cast<uint4*>(sh.q[i] + tile_chunk(c >> 3, row, c & 7)) =
+              make_uint4(half2_of(f[0], f[4]), half2_of(f[2], f[6]), half2_of(f[1], f[5]), half2_of(f[3], f[7]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full[i]);
+
+        // ---- limits of this row and of the row tile
+        // not zero: a masked score is -Inf before it is multiplied
+        const float factor = fmaxf(scale_exp2(a.scale * kg * kLog2e, 7 - ex), 1.17549435e-38f);
+        const int64_t pos0 = (int64_t)w.seq.len - w.seq.rows;
+        const int32_t r_last = (nrows - r0 < 128 ? nrows : r0 + 128) - 1;
+        const Visible first_row = visible(pos0 + r0 / a.group, w.seq.len, a.causal, a.window);
+        const Visible last_row = visible(pos0 + r_last / a.group, w.seq.len, a.causal, a.window);
+        Visible mine = visible(pos0 + r / a.group, w.seq.len, a.causal, a.window);
+        if (!live) mine = Visible{0, 0x7FFFFFFF};  // never written
+        const int32_t all_lo = last_row.lo, all_hi = first_row.hi;
+        const int32_t* table = a.ix.table + (int64_t)w.b * a.ix.width;
+        const int32_t gend = w.span.g0 + w.span.n;
+        // lanes 0..7: whether the page of granule g0 + 8j + lane is none
+        auto no_page = [&](int j) {
+          const int gi = w.span.g0 + kUnitGranules * j + (lane & 7);
+          const int32_t p = gi < gend ? table[gi / gpp] : 0;
+          return p < 0 || p >= a.ix.num_pages;
+        };
+        bool bad_next = w.span.n > 0 && no_page(j0);
+
+        float m = kStartMax, l = 0.0f;
+        for (int j = j0; j < j1; ++j) {
+          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, bad_next);
+          if (j + 1 < j1) bad_next = no_page(j + 1);
+          const int32_t tok0 = (w.span.g0 + kUnitGranules * j) * kGranule;
+          const bool whole = w.span.n > 0 && tok0 >= all_lo && tok0 + kTileTokens <= all_hi && bad == 0;
+          if (!(ok = wait(&sh.s_full[i], tiles & 1))) break;
+          tc_fence_after();
+          uint32_t p[64];
+          auto masked = [&](uint32_t (&s)[32], int c0) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int32_t tk = tok0 + c0 + e;
+              if (tk < mine.lo || tk >= mine.hi || ((bad >> ((c0 + e) >> 4)) & 1u)) s[e] = 0xFF800000u;
+            }
+          };
+          auto weights = [&](float mm) {  // p of the row's 128 tokens and their sum
+            const f32x2 ff = pack2(factor, factor), mm2 = pack2(-mm, -mm);
+            f32x2 sum = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              tmem_read32(t_s + 32 * c, s);
+              if (!whole) masked(s, 32 * c);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), ff, mm2), x, y);
+                x = ex2(x);
+                y = ex2(y);
+                sum = add2(sum, pack2(x, y));
+                p[16 * c + e] = half2_of(x, y);
+              }
+            }
+            float x, y;
+            unpack2(sum, x, y);
+            return x + y;
+          };
+          float sum = weights(m);
+          const bool grow = sum > kSumLimit;
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              tmem_read32(t_s + 32 * c, s);
+              if (!whole) masked(s, 32 * c);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(s[e]));
+            }
+            const float m1 = grow ? fmaxf(m, top * factor) : m;
+            const float f = m == kStartMax ? 0.0f : ex2(m - m1);
+            m = m1;
+            l *= f;
+            if (j > j0) {
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_read32(t_o + 32 * c, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(t_o + 32 * c, o);
+              }
+            }
+            sum = weights(m);
+          }
+          l += sum;
+          tmem_st32(t_s, p);
+          tmem_st32(t_s + 32, p + 32);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_full[i]);
+          ++tiles;
+        }
+        if (!ok) break;
+
+        // ---- epilogue: O of the last tile is complete
+        if (!(ok = wait(&sh.pv_done[i], (tiles - 1) & 1))) break;
+        tc_fence_after();
+        const bool whole_work = j0 == 0 && j1 == w.n;
+        const int64_t at = tok * a.ix.hkv * a.group + hq;
+        if (m == kStartMax) m = -INFINITY;
+        auto write_row = [&](int c, const float* o, float f) {  // 32 dimensions from 32*c, in the tile's order
+          uint4* out = reinterpret_cast<uint4*>(a.out + at * D + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float* x = o + 8 * e;
+            out[e] = make_uint4(f32x2_to_bf16x2(x[0] * f, x[4] * f), f32x2_to_bf16x2(x[2] * f, x[6] * f),
+                                f32x2_to_bf16x2(x[1] * f, x[5] * f), f32x2_to_bf16x2(x[3] * f, x[7] * f));
+          }
+        };
+        const bool write = live && NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status);
+        if (whole_work) {
+          const float f = l == 0.0f ? 0.0f : 128.0f * vg / l;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_read32(t_o + 32 * c, o);
+            if (write) write_row(c, reinterpret_cast<const float*>(o), f);
+          }
+          if (write && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+        } else {
+          // part of a work: m, l, then O in pieces of 4 columns x 128 rows
+          constexpr int kPart = 128 * (D + 2);
+          auto part_of = [&](int64_t cta, bool head_part) { return a.partial + ((2 * cta + head_part) * 2 + i) * kPart; };
+          float* mine_p = part_of(blockIdx.x, j0 == 0);
+          mine_p[row] = m;
+          mine_p[128 + row] = l;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_read32(t_o + 32 * c, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(mine_p + 256 + ((8 * c + e) * 128 + row) * 4) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          __threadfence();
+          if (!(ok = meet())) break;
+          const int64_t c0 = w.w0 / per, c1 = (w.w0 + w.n - 1) / per;
+          if (row == 0) {
+            const int last = atomicAdd(&a.counters[2 * c0 + i], 1) == (int)(c1 - c0);
+            if (last) a.counters[2 * c0 + i] = 0;
+            __threadfence();
+            sh.last[i] = last;
+          }
+          if (!(ok = meet())) break;
+          if (sh.last[i]) {
+            float mt = -INFINITY, lt = 0.0f;
+            for (int64_t c = c0; c <= c1; ++c) mt = fmaxf(mt, __ldcg(part_of(c, c == c0) + row));
+            for (int64_t c = c0; c <= c1; ++c) {
+              const float mc = __ldcg(part_of(c, c == c0) + row);
+              lt += mc == -INFINITY ? 0.0f : __ldcg(part_of(c, c == c0) + 128 + row) * ex2(mc - mt);
+            }
+            const float f = lt == 0.0f ? 0.0f : 128.0f * vg / lt;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+              for (int64_t x = c0; x <= c1; ++x) {
+                const float* from = part_of(x, x == c0);
+                const float mc = __ldcg(from + row);
+                const float g = mc == -INFINITY ? 0.0f : ex2(mc - mt);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 y = __ldcg(reinterpret_cast<const float4*>(from + 256 + ((8 * c + e) * 128 + row) * 4));
+                  o[4 * e] += y.x * g;
+                  o[4 * e + 1] += y.y * g;
+                  o[4 * e + 2] += y.z * g;
+                  o[4 * e + 3] += y.w * g;
+                }
+              }
+              if (write) write_row(c, o, f);
+            }
+            if (write && a.lse) a.lse[at] = lt == 0.0f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+          }
+          if (!(ok = meet())) break;  // sh.last is read before the next work writes it
+        }
+        tc_fence_before();
+      }
+      if (u >= u1 || !w.next(a)) break;
+    }
+    if (!ok) timed_out();
+  } else if (warp < 12) {
+    // ------------------------------------------------------ dequantization
+    regs_dec<104>();
+    const int dw = warp - 8;
+    uint32_t phase = 0, it = 0;   // ring parities; K/V tiles done
+    uint32_t in_flight = 0;       // ring stages with a copy that was not waited for
+    bool ok = true;
+    for (int64_t u = u0; ok;) {
+      const int j0 = from_unit(u), j1 = to_unit();
+      u = w.w0 + j1;
+      const int cnt = 2 * (j1 - j0);  // this warp's granules: 8*tile + dw and + 4
+      const int32_t* table = a.ix.table + (int64_t)w.b * a.ix.width;
+      auto granule = [&](int x) { return kUnitGranules * (j0 + (x >> 1)) + dw + 4 * (x & 1); };  // within the span
+      auto fetch_ids = [&](int x0) {
+        const int x = x0 + lane;
+        int32_t p = -1;
+        if (x < cnt && granule(x) < w.span.n) {
+          const int pi = (w.span.g0 + granule(x)) / gpp;
+          if (NVFP4_IN_BOUNDS(pi, a.ix.width, a.status)) p = table[pi];
+          if (p < 0 || p >= a.ix.num_pages) {
+            record_status(a.status, NVFP4_ERR_PAGE);
+            p = -1;
+          }
+        }
+        return p;
+      };
+      int32_t ids = -1, next_ids = -1;
+      auto issue = [&](int x) {
+        if ((x & 31) == 0) next_ids = fetch_ids(x);
+        const int32_t p = __shfl_sync(0xFFFFFFFFu, next_ids, x & 31);
+        if (p < 0) return;
+        const int gi = w.span.g0 + granule(x), st = x % kRing;
+        int64_t at = (((int64_t)p * a.ix.hkv + w.head) * gpp + gi % gpp) * kGB;
+        if (!NVFP4_IN_BOUNDS(at + kGB - 1, a.ix.num_pages * a.ix.hkv * gpp * kGB, a.status)) at = 0;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh.ring_full[dw][st], kGB);
+          bulk_load(sh.ring[dw][st], a.pages + at, kGB, &sh.ring_full[dw][st]);
+        }
+        in_flight |= 1u << st;
+      };
+      // K (which = 0) or V of granule x into rows 16*(its place in the tile) of an FP16 tile; zeros for none
+      auto expand = [&](int x, bool some, int which, uint8_t* tile) {
+        const uint8_t* gr = sh.ring[dw][x % kRing] + which * 9 * D;
+        const int r = (granule(x) % kUnitGranules) * kGranule + (lane >> 1);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {  // two lanes share the 64 dimensions of half h of a token
+          uint4 codes = make_uint4(0, 0, 0, 0);
+          uint32_t sc = 0;
+          if (some) {
+            codes = *reinterpret_cast<const uint4*>(gr + (lane >> 1) * (D / 2) + h * 32 + (lane & 1) * 16);
+            sc = *reinterpret_cast<const uint16_t*>(gr + 8 * D + (lane >> 1) * (D / 16) + h * 4 + (lane & 1) * 2);
+          }
+          const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t f = scales_to_half(__byte_perm(sc, 0, e < 2 ? 0x4040 : 0x4141));
+            uint32_t o[4];
+            codes_to_half(cw[e], o);
+            *reinterpret_cast<uint4*>(tile + tile_chunk(h, r, (lane & 1) * 4 + e)) =
+                make_uint4(hmul2(o[0], f), hmul2(o[1], f), hmul2(o[2], f), hmul2(o[3], f));
+          }
+        }
+      };
+      for (int x = 0; x < (cnt < kRing ? cnt : kRing); ++x) issue(x);
+      for (int x = 0; x < cnt; x += 2) {  // a tile: this warp's two granules
+        const uint32_t st = it & 1, par = (it >> 1) & 1;
+        if ((x & 31) == 0) ids = fetch_ids(x);
+        bool some[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          some[y] = __shfl_sync(0xFFFFFFFFu, ids, (x + y) & 31) >= 0;
+          if (some[y] && ok) {
+            const int rs = (x + y) % kRing;
+            ok = wait(&sh.ring_full[dw][rs], (phase >> rs) & 1u);
+            if (ok) {
+              phase ^= 1u << rs;
+              in_flight &= ~(1u << rs);
+            }
+          }
+        }
+        if (!ok || !(ok = wait(&sh.k_empty[st], par ^ 1))) break;
+        expand(x, some[0], 0, sh.k[st]);
+        expand(x + 1, some[1], 0, sh.k[st]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.k_full[st]);
+        if (!(ok = wait(&sh.v_empty[st], par ^ 1))) break;
+        expand(x, some[0], 1, sh.v[st]);
+        expand(x + 1, some[1], 1, sh.v[st]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_full[st]);
+        for (int y = 0; y < 2; ++y)
+          if (x + y + kRing < cnt) issue(x + y + kRing);
+        ++it;
+      }
+      if (!ok || u >= u1 || !w.next(a)) break;
+    }
+    if (!ok) {
+      timed_out();
+      // copies in flight land before the CTA exits (bounded)
+      for (int rs = 0; rs < kRing; ++rs) {
+        if (!((in_flight >> rs) & 1u)) continue;
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&sh.ring_full[dw][rs], (phase >> rs) & 1u) && globaltimer_ns() - t0 < 1000000ull) {
+        }
+      }
+    }
+  } else {
+    // ----------------------------------------------------------- MMA issue
+    regs_dec<72>();
+    if (warp < 14) {
+      const int i = warp - 12;
+      constexpr uint32_t idesc_s = idesc_f16(kTileTokens, false), idesc_o = idesc_f16(D, true);
+      const uint32_t t_s = tmem + i * 128, t_o = tmem + 256 + i * D;
+      uint32_t it = 0, tiles = 0, works = 0;
+      bool ok = true;
+      auto scores = [&](uint32_t t) {  // S = Q K^T of K/V tile t
+        const uint32_t st = t & 1;
+        if (!wait(&sh.k_full[st], (t >> 1) & 1)) return false;
+        tc_fence_after();
+        const uint64_t qd = smem_desc(smem_u32(sh.q[i]), 16, 1024, 2), kd = smem_desc(smem_u32(sh.k[st]), 16, 1024, 2);
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk) {  // 32 bytes within a 64-dimension half, halves 16 KB apart
+          const uint64_t off = (uint64_t)((kk & 3) * 2 + (kk >> 2) * (kTileTokens * 128 / 16));
+          mma_f16_ss_elect(t_s, qd + off, kd + off, idesc_s, kk != 0);
+        }
+        tc_commit_elect(&sh.s_full[i]);
+        tc_commit_elect(&sh.k_empty[st]);
+        return true;
+      };
+      for (int64_t u = u0; ok;) {
+        const int j0 = from_unit(u), j1 = to_unit();
+        u = w.w0 + j1;
+        const int n = j1 - j0;
+        if (w.tile * kPreRows + i * 128 < w.seq.rows * a.group) {
+          if (!(ok = wait(&sh.q_full[i], works & 1))) break;
+          ++works;
+          tc_fence_after();
+          if (!(ok = scores(it))) break;
+          for (int j = 0; j < n; ++j, ++it, ++tiles) {
+            const uint32_t st = it & 1;
+            if (!(ok = wait(&sh.v_full[st], (it >> 1) & 1))) break;
+            if (!(ok = wait(&sh.p_full[i], tiles & 1))) break;
+            tc_fence_after();
+            const uint64_t vd = smem_desc(smem_u32(sh.v[st]), kTileTokens * 128, 1024, 2);
+#pragma unroll
+            for (int kk = 0; kk < kTileTokens / 16; ++kk)  // 16 tokens: two groups of eight rows of 128 bytes
+              mma_f16_ts_elect(t_o, t_s + 8 * kk, vd + (uint64_t)(kk * 2048 / 16), idesc_o, (j | kk) != 0);
+            tc_commit_elect(&sh.pv_done[i]);
+            tc_commit_elect(&sh.v_empty[st]);
+            if (!(ok = wait(&sh.pv_done[i], tiles & 1))) break;
+            if (j + 1 < n && !(ok = scores(it + 1))) break;
+          }
+        } else {  // no rows in this half: the stages are only passed on
+          for (int j = 0; j < n && ok; ++j, ++it) {
+            const uint32_t st = it & 1;
+            ok = wait(&sh.k_full[st], (it >> 1) & 1) && wait(&sh.v_full[st], (it >> 1) & 1);
+            if (ok && lane == 0) {
+              mbar_arrive(&sh.k_empty[st]);
+              mbar_arrive(&sh.v_empty[st]);
+            }
+            __syncwarp();
+          }
+        }
+        if (!ok || u >= u1 || !w.next(a)) break;
+      }
+      if (!ok) {
+        timed_out();
+        if (lane == 0) {  // MMAs in flight read shared memory: a grace time, then the CTA may exit
+          const uint64_t t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 1000000ull) {
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr int kMaxPreCtas = 160;
+
+size_t kv_prefill_partial_floats() { return (size_t)kMaxPreCtas * 4 * 128 * (128 + 2); }
+
+template <int D>
+cudaError_t launch_tiles(const AttnArgs& a, int num_sms, cudaStream_t s) {
+  constexpr int bytes = (int)sizeof(PreShared<D>) + 1024;
+  static_assert(bytes <= 232448, "shared memory budget");
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (attr != cudaSuccess) return attr;
+  note_launch();
+  kv_prefill_kernel<D><<<num_sms < kMaxPreCtas ? num_sms : kMaxPreCtas, kPreThreads, bytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_prefill(const AttnArgs& a, int D, int num_sms, cudaStream_t s) {
+  return D == 128 ? launch_tiles<128>(a, num_sms, s) : launch_tiles<64>(a, num_sms, s);
+}
+
+}  // namespace nvfp4
