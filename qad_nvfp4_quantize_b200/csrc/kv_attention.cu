@@ -34,7 +34,6 @@ namespace nvfp4 {
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr float kRescaleAt = 8.0f;
 
 template <int D, int NT>
 struct AttnShared {
@@ -143,23 +142,14 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
       const int ex = query_exponent(__uint_as_float(mx << 16));
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) {  // eight dimensions: pairs (0,4), (2,6), (1,5), (3,7) as codes_to_half
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[2 * e] = scale_exp2(__uint_as_float(raw[4 * w + e] << 16), ex);
-          f[2 * e + 1] = scale_exp2(__uint_as_float(raw[4 * w + e] & 0xFFFF0000u), ex);
-        }
-        qf[nt][4 * w] = half2_bits(f[0], f[4]);
-        qf[nt][4 * w + 1] = half2_bits(f[2], f[6]);
-        qf[nt][4 * w + 2] = half2_bits(f[1], f[5]);
-        qf[nt][4 * w + 3] = half2_bits(f[3], f[7]);
-      }
+      for (int e = 0; e < 4 * kWords; ++e)
+        qf[nt][e] = half2_bits(scale_exp2(__uint_as_float(raw[e] << 16), ex),
+                               scale_exp2(__uint_as_float(raw[e] & 0xFFFF0000u), ex));
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int64_t rc = (int64_t)tile * kRows + 8 * nt + 2 * t + c;
         const int ec = __shfl_sync(0xFFFFFFFFu, ex, (2 * t + c) * 4);
-        factor[nt][c] = scale_exp2(a.scale * kg * kLog2e, 7 - ec);
+        factor[nt][c] = scale_exp2(a.scale * kg * kLog2e, kValueExp - ec);
         Visible v{0, 0};
         if (rc < nrows) v = visible((int64_t)seq.len - seq.rows + rc / a.group, seq.len, a.causal, a.window);
         lo[nt][c] = v.lo;
@@ -357,20 +347,19 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
           f[k] = scales_to_half(x | (y << 16));
         }
 #pragma unroll
-        for (int i2 = 0; i2 < 2 * kVWords; ++i2) {  // four dimensions of the lane's run at a time
-          uint32_t pa[4], pb[4];
-          const uint32_t sel = (i2 & 1) ? 0x7632 : 0x5410;
-          codes_to_half(__byte_perm(w[0][i2 >> 1], w[1][i2 >> 1], sel), pa);
-          codes_to_half(__byte_perm(w[2][i2 >> 1], w[3][i2 >> 1], sel), pb);
+        for (int x = 0; x < kVWords; ++x) {  // eight dimensions of the lane's run at a time
+          // the tokens' nibbles side by side: even dimensions, then odd ones, of two tokens in each byte
+          uint32_t pa[2][4], pb[2][4];
+          codes_to_half((w[0][x] & 0x0F0F0F0Fu) | ((w[1][x] << 4) & 0xF0F0F0F0u), pa[0]);
+          codes_to_half(((w[0][x] >> 4) & 0x0F0F0F0Fu) | (w[1][x] & 0xF0F0F0F0u), pa[1]);
+          codes_to_half((w[2][x] & 0x0F0F0F0Fu) | ((w[3][x] << 4) & 0xF0F0F0F0u), pb[0]);
+          codes_to_half(((w[2][x] >> 4) & 0x0F0F0F0Fu) | (w[3][x] & 0xF0F0F0F0u), pb[1]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            pa[e] = hmul2(pa[e], f[0]);
-            pb[e] = hmul2(pb[e], f[1]);
-          }
+          for (int e = 0; e < 4; ++e) {  // m-tile: dimensions 8x + 2e (rows 0..7) and 8x + 2e + 1 (rows 8..15)
+            const uint32_t a0 = hmul2(pa[0][e], f[0]), a1 = hmul2(pa[1][e], f[0]);
+            const uint32_t a2 = hmul2(pb[0][e], f[1]), a3 = hmul2(pb[1][e], f[1]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_16816(o[nt][2 * i2], pa[0], pa[2], pb[0], pb[2], pf[nt][0], pf[nt][1]);
-            mma_16816(o[nt][2 * i2 + 1], pa[1], pa[3], pb[1], pb[3], pf[nt][0], pf[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][4 * x + e], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
           }
         }
       }
@@ -426,7 +415,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
         const int64_t tok = seq.row0 + r / a.group, hq = (int64_t)head * a.group + r % a.group;
         const int64_t at = tok * a.ix.hkv * a.group + hq;
         const float lt = sh.l[row];
-        const float f = lt == 0.0f ? 0.0f : 128.0f * vg / lt;  // no visible token: zeros
+        const float f = lt == 0.0f ? 0.0f : kValueScale * vg / lt;  // no visible token: zeros
         const float2 x = value(row, d);
         if (!NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status)) continue;
         *reinterpret_cast<uint32_t*>(a.out + at * D + d) = f32x2_to_bf16x2(x.x * f, x.y * f);

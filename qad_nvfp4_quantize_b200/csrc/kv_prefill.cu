@@ -13,7 +13,8 @@
 //                      epilogue;
 //   warps 8..11        dequantization: each keeps bulk copies of its granules
 //                      in flight (ring of kRing) and writes K and V as FP16
-//                      rows of 64 dimensions, 128-byte swizzled, two stages;
+//                      rows of 64 dimensions, 128-byte swizzled, into a ring
+//                      of three tiles (K0 V0 K1 V1 ...);
 //   warps 12, 13       issue the MMAs of row tile 0 and 1: S = Q K^T (K-major
 //                      operands), O += P V (P from tensor memory, V read with
 //                      its 64-dimension runs as the MN-major operand).
@@ -23,12 +24,9 @@
 // of this one is complete (its columns hold P), which also means that O is at
 // rest whenever a softmax warp has scores to look at: it rescales O by itself.
 //
-// The running maximum m is allowed to lag: a row keeps m while the sum of its
-// tile's p stays below 2^14 (then every p fits FP16) and takes the true maximum
-// otherwise, so the usual tile needs no maximum at all.
-//
-// Head dimensions are stored in the order in which codes_to_half yields them
-// (0,4,2,6,1,5,3,7 of each eight), in Q as in K; the epilogue restores V's.
+// The running maximum m is allowed to lag by 8 (in log2 units): a row takes a
+// new one, and O is rescaled, only when a score exceeds it by more, so that p
+// stays below 2^8 and most tiles leave O alone.
 #include <cuda_fp16.h>
 
 #include "kv_attention.cuh"
@@ -40,21 +38,21 @@ constexpr int kPreRows = 256;
 constexpr int kTileTokens = 128;
 constexpr int kUnitGranules = kTileTokens / kGranule;
 constexpr float kStartMax = -1e30f;  // m before the first visible token, in log2 units
-constexpr float kSumLimit = 16384.0f;
 
 template <int D>
 struct PreShared {
-  static constexpr int kRing = 3;
+  static constexpr int kRing = 7;
+  static constexpr int kTiles = 3;
   static constexpr int kTile = kTileTokens * D * 2;  // bytes of an FP16 tile
-  uint8_t k[2][kTile];
-  uint8_t v[2][kTile];
+  uint8_t kv[kTiles][kTile];                         // K and V tiles in turn: K0 V0 K1 V1 ...
   union {
     uint8_t q[2][kTile];
     PartShared part;
   };
   uint8_t ring[4][kRing][granule_bytes(D)];
   uint64_t ring_full[4][kRing];
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2], group[2];
+  uint64_t full[kTiles], empty[kTiles];
+  uint64_t q_full[2], s_full[2], p_low[2], p_full[2], pv_done[2], turn[2], group[2];
   uint32_t tmem;
   int last[2];
   volatile int abort;
@@ -74,30 +72,67 @@ NVFP4_DEVINL void mma_f16_ts_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t 
                "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;" NVFP4_ELECT_END
                ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
-// 32 columns of this warp's 32 tensor-memory lanes, with the wait: one statement, so that the compiler moves or spills
-// no register of a load that is still under way.
-NVFP4_DEVINL void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
+// Columns of this warp's 32 tensor-memory lanes, with the wait: one statement,
+// so that the compiler moves or spills no register of a load under way.
+NVFP4_DEVINL void tmem_read16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
-NVFP4_DEVINL void tmem_st32(uint32_t taddr, const uint32_t* r) {
+NVFP4_DEVINL void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+NVFP4_DEVINL void tmem_read64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
+NVFP4_DEVINL void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+NVFP4_DEVINL void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
       "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 NVFP4_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -108,6 +143,11 @@ NVFP4_DEVINL void regs_inc() {
 template <int kRegs>
 NVFP4_DEVINL void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+NVFP4_DEVINL float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 NVFP4_DEVINL f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
@@ -140,15 +180,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   if (tid == 0) {
     for (int w = 0; w < 4; ++w)
       for (int i = 0; i < kRing; ++i) mbar_init(&sh.ring_full[w][i], 1);
+    for (int i = 0; i < Sh::kTiles; ++i) {
+      mbar_init(&sh.full[i], 4);
+      mbar_init(&sh.empty[i], 2);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 4);
-      mbar_init(&sh.k_full[i], 4);
-      mbar_init(&sh.v_full[i], 4);
-      mbar_init(&sh.k_empty[i], 2);
-      mbar_init(&sh.v_empty[i], 2);
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_low[i], 4);
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.turn[i], 4);
       mbar_init(&sh.group[i], 4);
     }
     sh.abort = 0;
@@ -177,19 +219,22 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     if (lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, &sh.abort, kAttnWaitNs); };
+  // place of K (2t) or V (2t + 1) in the ring of tiles, and the parity of its turn there
+  auto place = [](uint32_t x) { return x % Sh::kTiles; };
+  auto turn_of = [](uint32_t x) { return (x / Sh::kTiles) & 1; };
   // unit range of this CTA within the work
   auto from_unit = [&](int64_t u) { return (int)(u - w.w0); };
   auto to_unit = [&]() { return (int)(u1 - w.w0 < w.n ? u1 - w.w0 : (int64_t)w.n); };
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax
-    regs_inc<168>();  // 2 * 168 + 104 + 72 = 4 * 128, what the block was launched with
+    regs_inc<152>();  // 2 * 152 + 104 + 104 = 4 * 128, what the block was launched with
     const int i = warp >> 2, wq = warp & 3, row = tid & 127;
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
     const uint32_t t_s = tmem + lane_base + i * 128, t_o = tmem + lane_base + 256 + i * D;
     const float kg = *a.k_g, vg = *a.v_g;
     uint32_t tiles = 0;  // tiles done by this row tile
-    uint32_t meets = 0;
+    uint32_t meets = 0, turns = 0;
     auto meet = [&]() {  // the four warps of the row tile, with the usual bound
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.group[i]);
@@ -218,23 +263,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         for (int c = 0; c < D / 8; ++c) {
           uint4 x = make_uint4(0, 0, 0, 0);
           if (live) x = ld_stream(q4 + c);
-          float f[8];
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[2 * e] = scale_exp2(__uint_as_float(xs[e] << 16), ex);
-            f[2 * e + 1] = scale_exp2(__uint_as_float(xs[e] & 0xFFFF0000u), ex);
-          }
+          auto two = [&](uint32_t b) {
+            return half2_of(scale_exp2(__uint_as_float(b << 16), ex), scale_exp2(__uint_as_float(b & 0xFFFF0000u), ex));
+          };
           *reinterpret_cast<uint4*>(sh.q[i] + tile_chunk(c >> 3, row, c & 7)) =
-              make_uint4(half2_of(f[0], f[4]), half2_of(f[2], f[6]), half2_of(f[1], f[5]), half2_of(f[3], f[7]));
+              make_uint4(two(x.x), two(x.y), two(x.z), two(x.w));
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full[i]);
 
+        const bool both = w.tile * kPreRows + 128 < nrows;  // the other row tile has rows too
         // ---- limits of this row and of the row tile
         // not zero: a masked score is -Inf before it is multiplied
-        const float factor = fmaxf(scale_exp2(a.scale * kg * kLog2e, 7 - ex), 1.17549435e-38f);
+        const float factor = fmaxf(scale_exp2(a.scale * kg * kLog2e, kValueExp - ex), 1.17549435e-38f);
         const int64_t pos0 = (int64_t)w.seq.len - w.seq.rows;
         const int32_t r_last = (nrows - r0 < 128 ? nrows : r0 + 128) - 1;
         const Visible first_row = visible(pos0 + r0 / a.group, w.seq.len, a.causal, a.window);
@@ -260,71 +302,91 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           const bool whole = w.span.n > 0 && tok0 >= all_lo && tok0 + kTileTokens <= all_hi && bad == 0;
           if (!(ok = wait(&sh.s_full[i], tiles & 1))) break;
           tc_fence_after();
-          uint32_t p[64];
-          auto masked = [&](uint32_t (&s)[32], int c0) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int32_t tk = tok0 + c0 + e;
-              if (tk < mine.lo || tk >= mine.hi || ((bad >> ((c0 + e) >> 4)) & 1u)) s[e] = 0xFF800000u;
-            }
-          };
-          auto weights = [&](float mm) {  // p of the row's 128 tokens and their sum
-            const f32x2 ff = pack2(factor, factor), mm2 = pack2(-mm, -mm);
-            f32x2 sum = 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t s[32];
-              tmem_read32(t_s + 32 * c, s);
-              if (!whole) masked(s, 32 * c);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float x, y;
-                unpack2(fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), ff, mm2), x, y);
-                x = ex2(x);
-                y = ex2(y);
-                sum = add2(sum, pack2(x, y));
-                p[16 * c + e] = half2_of(x, y);
-              }
-            }
-            float x, y;
-            unpack2(sum, x, y);
-            return x + y;
-          };
-          float sum = weights(m);
-          const bool grow = sum > kSumLimit;
-          if (__any_sync(0xFFFFFFFFu, grow)) {
-            float top = -INFINITY;
+          if (!whole) {  // what a row does not see becomes -Inf in place
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t s[32];
-              tmem_read32(t_s + 32 * c, s);
-              if (!whole) masked(s, 32 * c);
+            for (int c = 0; c < 8; ++c) {
+              uint32_t x[16];
+              tmem_read16(t_s + 16 * c, x);
+              const int32_t t0 = tok0 + 16 * c;
+              const bool none = (bad >> c) & 1u;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(s[e]));
+              for (int e = 0; e < 16; ++e)
+                if (none || t0 + e < mine.lo || t0 + e >= mine.hi) x[e] = 0xFF800000u;
+              tmem_st16(t_s + 16 * c, x);
             }
-            const float m1 = grow ? fmaxf(m, top * factor) : m;
+            tmem_wait_st();
+          }
+          // the row's maximum: columns 64..127 are read again below, 0..63 stay in registers
+          uint32_t x[64];
+          auto largest = [&]() {
+            float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
+#pragma unroll
+            for (int e = 0; e < 64; e += 8) {
+              t0 = max3(t0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              t1 = max3(t1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+              t2 = max3(t2, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
+              t3 = max3(t3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
+            }
+            return max3(fmaxf(t0, t1), t2, t3);
+          };
+          tmem_read64(t_s + 64, x);
+          float top = largest();
+          tmem_read64(t_s, x);
+          top = fmaxf(top, largest()) * factor;
+          if (__any_sync(0xFFFFFFFFu, top > m + kRescaleAt)) {
+            const float m1 = fmaxf(m, top);
             const float f = m == kStartMax ? 0.0f : ex2(m - m1);
             m = m1;
             l *= f;
             if (j > j0) {
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_read32(t_o + 32 * c, o);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_read16(t_o + 16 * c, o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(t_o + 32 * c, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(t_o + 16 * c, o);
               }
             }
-            sum = weights(m);
           }
-          l += sum;
-          tmem_st32(t_s, p);
-          tmem_st32(t_s + 32, p + 32);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_full[i]);
+          // p of 64 columns as FP16 pairs into 32 columns whose scores have been read
+          f32x2 sum = 0;
+          const f32x2 ff = pack2(factor, factor), mm = pack2(-m, -m);
+          auto weights = [&](uint32_t to, uint64_t* bar) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t p[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float a0, a1;
+                unpack2(fma2(pack2(__uint_as_float(x[32 * c + 2 * e]), __uint_as_float(x[32 * c + 2 * e + 1])), ff, mm),
+                        a0, a1);
+                a0 = ex2(a0);
+                a1 = ex2(a1);
+                sum = add2(sum, pack2(a0, a1));
+                p[e] = half2_of(a0, a1);
+              }
+              tmem_st16(to + 16 * c, p);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+          };
+          // the two row tiles take turns at the 2^x unit: while one computes weights the tensor pipe has the other
+          if (both && !(ok = wait(&sh.turn[i], (turns & 1) ^ (i == 0 ? 1 : 0)))) break;
+          weights(t_s, &sh.p_low[i]);
+          tmem_read64(t_s + 64, x);
+          weights(t_s + 32, &sh.p_full[i]);
+          if (both) {
+            if (lane == 0) mbar_arrive(&sh.turn[1 - i]);
+            ++turns;
+          }
+          {
+            float s0, s1;
+            unpack2(sum, s0, s1);
+            l += s0 + s1;
+          }
           ++tiles;
         }
         if (!ok) break;
@@ -335,18 +397,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         const bool whole_work = j0 == 0 && j1 == w.n;
         const int64_t at = tok * a.ix.hkv * a.group + hq;
         if (m == kStartMax) m = -INFINITY;
-        auto write_row = [&](int c, const float* o, float f) {  // 32 dimensions from 32*c, in the tile's order
+        auto write_row = [&](int c, const float* o, float f) {  // 32 dimensions from 32*c
           uint4* out = reinterpret_cast<uint4*>(a.out + at * D + 32 * c);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float* x = o + 8 * e;
-            out[e] = make_uint4(f32x2_to_bf16x2(x[0] * f, x[4] * f), f32x2_to_bf16x2(x[2] * f, x[6] * f),
-                                f32x2_to_bf16x2(x[1] * f, x[5] * f), f32x2_to_bf16x2(x[3] * f, x[7] * f));
+            out[e] = make_uint4(f32x2_to_bf16x2(x[0] * f, x[1] * f), f32x2_to_bf16x2(x[2] * f, x[3] * f),
+                                f32x2_to_bf16x2(x[4] * f, x[5] * f), f32x2_to_bf16x2(x[6] * f, x[7] * f));
           }
         };
         const bool write = live && NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status);
         if (whole_work) {
-          const float f = l == 0.0f ? 0.0f : 128.0f * vg / l;
+          const float f = l == 0.0f ? 0.0f : kValueScale * vg / l;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -387,7 +449,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
               const float mc = __ldcg(part_of(c, c == c0) + row);
               lt += mc == -INFINITY ? 0.0f : __ldcg(part_of(c, c == c0) + 128 + row) * ex2(mc - mt);
             }
-            const float f = lt == 0.0f ? 0.0f : 128.0f * vg / lt;
+            const float f = lt == 0.0f ? 0.0f : kValueScale * vg / lt;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               float o[32];
@@ -482,7 +544,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       };
       for (int x = 0; x < (cnt < kRing ? cnt : kRing); ++x) issue(x);
       for (int x = 0; x < cnt; x += 2) {  // a tile: this warp's two granules
-        const uint32_t st = it & 1, par = (it >> 1) & 1;
         if ((x & 31) == 0) ids = fetch_ids(x);
         bool some[2];
 #pragma unroll
@@ -497,18 +558,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
             }
           }
         }
-        if (!ok || !(ok = wait(&sh.k_empty[st], par ^ 1))) break;
-        expand(x, some[0], 0, sh.k[st]);
-        expand(x + 1, some[1], 0, sh.k[st]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.k_full[st]);
-        if (!(ok = wait(&sh.v_empty[st], par ^ 1))) break;
-        expand(x, some[0], 1, sh.v[st]);
-        expand(x + 1, some[1], 1, sh.v[st]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.v_full[st]);
+        for (uint32_t which = 0; ok && which < 2; ++which) {
+          const uint32_t tile = 2 * it + which;
+          if (!(ok = wait(&sh.empty[place(tile)], turn_of(tile) ^ 1))) break;
+          expand(x, some[0], which, sh.kv[place(tile)]);
+          expand(x + 1, some[1], which, sh.kv[place(tile)]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[place(tile)]);
+        }
+        if (!ok) break;
         for (int y = 0; y < 2; ++y)
           if (x + y + kRing < cnt) issue(x + y + kRing);
         ++it;
@@ -527,7 +586,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     }
   } else {
     // ----------------------------------------------------------- MMA issue
-    regs_dec<72>();
+    regs_dec<104>();
     if (warp < 14) {
       const int i = warp - 12;
       constexpr uint32_t idesc_s = idesc_f16(kTileTokens, false), idesc_o = idesc_f16(D, true);
@@ -535,17 +594,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       uint32_t it = 0, tiles = 0, works = 0;
       bool ok = true;
       auto scores = [&](uint32_t t) {  // S = Q K^T of K/V tile t
-        const uint32_t st = t & 1;
-        if (!wait(&sh.k_full[st], (t >> 1) & 1)) return false;
+        const uint32_t st = place(2 * t);
+        if (!wait(&sh.full[st], turn_of(2 * t))) return false;
         tc_fence_after();
-        const uint64_t qd = smem_desc(smem_u32(sh.q[i]), 16, 1024, 2), kd = smem_desc(smem_u32(sh.k[st]), 16, 1024, 2);
+        const uint64_t qd = smem_desc(smem_u32(sh.q[i]), 16, 1024, 2), kd = smem_desc(smem_u32(sh.kv[st]), 16, 1024, 2);
 #pragma unroll
         for (int kk = 0; kk < kSteps; ++kk) {  // 32 bytes within a 64-dimension half, halves 16 KB apart
           const uint64_t off = (uint64_t)((kk & 3) * 2 + (kk >> 2) * (kTileTokens * 128 / 16));
           mma_f16_ss_elect(t_s, qd + off, kd + off, idesc_s, kk != 0);
         }
         tc_commit_elect(&sh.s_full[i]);
-        tc_commit_elect(&sh.k_empty[st]);
+        tc_commit_elect(&sh.empty[st]);
         return true;
       };
       for (int64_t u = u0; ok;) {
@@ -558,26 +617,30 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           tc_fence_after();
           if (!(ok = scores(it))) break;
           for (int j = 0; j < n; ++j, ++it, ++tiles) {
-            const uint32_t st = it & 1;
-            if (!(ok = wait(&sh.v_full[st], (it >> 1) & 1))) break;
-            if (!(ok = wait(&sh.p_full[i], tiles & 1))) break;
-            tc_fence_after();
-            const uint64_t vd = smem_desc(smem_u32(sh.v[st]), kTileTokens * 128, 1024, 2);
+            const uint32_t st = place(2 * it + 1);
+            if (!(ok = wait(&sh.full[st], turn_of(2 * it + 1)))) break;
+            const uint64_t vd = smem_desc(smem_u32(sh.kv[st]), kTileTokens * 128, 1024, 2);
 #pragma unroll
-            for (int kk = 0; kk < kTileTokens / 16; ++kk)  // 16 tokens: two groups of eight rows of 128 bytes
-              mma_f16_ts_elect(t_o, t_s + 8 * kk, vd + (uint64_t)(kk * 2048 / 16), idesc_o, (j | kk) != 0);
+            for (int half = 0; half < 2; ++half) {
+              if (!(ok = wait(half ? &sh.p_full[i] : &sh.p_low[i], tiles & 1))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k4 = 0; k4 < 4; ++k4) {  // 16 tokens: two groups of eight rows of 128 bytes
+                const int kk = 4 * half + k4;
+                mma_f16_ts_elect(t_o, t_s + 8 * kk, vd + (uint64_t)(kk * 2048 / 16), idesc_o, (j | kk) != 0);
+              }
+            }
+            if (!ok) break;
             tc_commit_elect(&sh.pv_done[i]);
-            tc_commit_elect(&sh.v_empty[st]);
+            tc_commit_elect(&sh.empty[st]);
             if (!(ok = wait(&sh.pv_done[i], tiles & 1))) break;
             if (j + 1 < n && !(ok = scores(it + 1))) break;
           }
         } else {  // no rows in this half: the stages are only passed on
           for (int j = 0; j < n && ok; ++j, ++it) {
-            const uint32_t st = it & 1;
-            ok = wait(&sh.k_full[st], (it >> 1) & 1) && wait(&sh.v_full[st], (it >> 1) & 1);
-            if (ok && lane == 0) {
-              mbar_arrive(&sh.k_empty[st]);
-              mbar_arrive(&sh.v_empty[st]);
+            for (uint32_t tile = 2 * it; ok && tile < 2 * it + 2; ++tile) {
+              ok = wait(&sh.full[place(tile)], turn_of(tile));
+              if (ok && lane == 0) mbar_arrive(&sh.empty[place(tile)]);
             }
             __syncwarp();
           }
