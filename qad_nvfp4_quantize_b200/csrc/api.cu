@@ -303,7 +303,8 @@ nvfp4_status nvfp4_kv_append(const void* k, const void* v, int64_t row_stride, i
   DeviceInfo* d;
   nvfp4_status st = current_device(&d);
   if (st != NVFP4_OK) return st;
-  const nvfp4::KvIndex ix{cu_q, kv_len, block_table, batch, table_width, page_size, kv_heads, total, num_pages};
+  const nvfp4::KvIndex ix{cu_q, kv_len, block_table, batch, table_width, page_size, kv_heads, total, num_pages,
+                           __builtin_ctz(page_size / nvfp4::kGranule)};
   return launched(nvfp4::launch_kv_append(k, v, row_stride, head_dim, ix, pages, k_g, v_g,
                                           mode == NVFP4_MODE_FOUR_OVER_SIX, d->status, d->num_sms,
                                           reinterpret_cast<cudaStream_t>(stream)));
@@ -334,7 +335,8 @@ nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_stride, int64_t tota
   nvfp4::AttnArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_stride;
-  a.ix = nvfp4::KvIndex{cu_q, kv_len, block_table, batch, table_width, page_size, kv_heads, total, num_pages};
+  a.ix = nvfp4::KvIndex{cu_q, kv_len, block_table, batch, table_width, page_size, kv_heads, total, num_pages,
+                           __builtin_ctz(page_size / nvfp4::kGranule)};
   a.pages = pages;
   a.k_g = k_g;
   a.v_g = v_g;

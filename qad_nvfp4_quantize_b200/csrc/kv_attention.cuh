@@ -91,7 +91,8 @@ struct AttnArgs {
 };
 
 
-constexpr uint64_t kAttnWaitNs = 2000000000ull;  // bound of every wait
+constexpr uint64_t kAttnWaitNs = 2000000000ull;     // bound of every wait: 2 s,
+constexpr int64_t kAttnWaitCycles = 4000000000ll;  // or its cycles
 constexpr float kRescaleAt = 8.0f;                // lag of the running maximum, in log2 units
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 

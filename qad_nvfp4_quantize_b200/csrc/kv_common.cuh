@@ -30,6 +30,7 @@ struct KvIndex {
   int batch, width, page, hkv;
   int64_t total;      // rows of the new-token tensors
   int64_t num_pages;
+  int gshift;         // log2 of the granules in a page
 };
 
 // Rows and cached length of a sequence, brought into the tensors' extents. A

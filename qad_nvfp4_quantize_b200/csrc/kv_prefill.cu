@@ -53,6 +53,8 @@ struct PreShared {
   uint64_t ring_full[4][kRing];
   uint64_t full[kTiles], empty[kTiles];
   uint64_t q_full[2], s_full[2], p_low[2], p_full[2], pv_done[2], turn[2], group[2];
+  WorkCursor<kPreRows, kUnitGranules> cursor[kPreThreads / 32];  // one per warp: no register is spent on it
+  int64_t u1, per;
   uint32_t tmem;
   int last[2];
   volatile int abort;
@@ -62,15 +64,82 @@ struct PreShared {
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-NVFP4_DEVINL void mma_f16_ss_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(NVFP4_ELECT_BEGIN ".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;" NVFP4_ELECT_END
-               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+// A run of MMAs and the commits behind it, issued by one elected lane of a
+// converged warp: one statement, because electing and setting up each
+// instruction by itself took the issuing warp 70 cycles, longer than the tensor
+// pipe needs for it.
+// S[tmem] = Q K^T over D dimensions: 32 bytes a step within a 64-dimension
+// half, halves 16 KB (1024 descriptor units) apart. Then arrives on both
+// barriers when all of the thread's MMAs are complete.
+template <int D>
+NVFP4_DEVINL void mma_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc, uint64_t* bar0, uint64_t* bar1) {
+  if constexpr (D == 128)
+    asm volatile(
+      "{\n\t.reg .pred e, t, z;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 z, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
+      "}"
+      ::"r"(d), "l"(q), "l"(k), "r"(idesc), "r"(smem_u32(bar0)), "r"(smem_u32(bar1))
+      : "memory");
+  else
+    asm volatile(
+      "{\n\t.reg .pred e, t, z;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 z, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
+      "}"
+      ::"r"(d), "l"(q), "l"(k), "r"(idesc), "r"(smem_u32(bar0)), "r"(smem_u32(bar1))
+      : "memory");
 }
-NVFP4_DEVINL void mma_f16_ts_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(NVFP4_ELECT_BEGIN ".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;" NVFP4_ELECT_END
-               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+// O[tmem] (+)= P V of 64 tokens: P in 8 columns a step, V in two groups of
+// eight rows of 128 bytes.
+NVFP4_DEVINL void mma_values(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, t, z;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 z, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, z;\n\t"
+      "add.s32 c, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t"
+      "add.s32 c, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t"
+      "add.s32 c, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t"
+      "}"
+      ::"r"(d), "r"(p), "l"(v), "r"(idesc), "r"(acc)
+      : "memory");
+}
+NVFP4_DEVINL void commit_two(uint64_t* bar0, uint64_t* bar1) {
+  asm volatile(
+      "{\n\t.reg .pred e, t, z;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t"
+      "}"
+      ::"r"(smem_u32(bar0)), "r"(smem_u32(bar1))
+      : "memory");
 }
 // Columns of this warp's 32 tensor-memory lanes, with the wait: one statement,
 // so that the compiler moves or spills no register of a load under way.
@@ -124,26 +193,7 @@ NVFP4_DEVINL void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-NVFP4_DEVINL void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
-      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 NVFP4_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-template <int kRegs>
-NVFP4_DEVINL void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-NVFP4_DEVINL void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
 NVFP4_DEVINL float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -163,6 +213,7 @@ NVFP4_DEVINL uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+NVFP4_DEVINL int uniform(int v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
 // Byte of 16-byte chunk c (0..7) of row r of half h (64 dimensions) in a 128-byte-swizzled tile.
 NVFP4_DEVINL uint32_t tile_chunk(int h, int r, int c) {
   return (uint32_t)(h * kTileTokens * 128 + r * 128 + ((c ^ (r & 7)) << 4));
@@ -171,11 +222,10 @@ NVFP4_DEVINL uint32_t tile_chunk(int h, int r, int c) {
 template <int D>
 __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnArgs a) {
   using Sh = PreShared<D>;
-  constexpr int kGB = granule_bytes(D), kRing = Sh::kRing, kSteps = D / 16;
+  constexpr int kGB = granule_bytes(D), kRing = Sh::kRing;
   extern __shared__ uint8_t pre_smem[];
   Sh& sh = *reinterpret_cast<Sh*>((reinterpret_cast<uintptr_t>(pre_smem) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gpp = a.ix.page / kGranule;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
 
   if (tid == 0) {
     for (int w = 0; w < 4; ++w)
@@ -202,10 +252,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     return per * blockIdx.x;
   };
   find_part<kPreRows, kUnitGranules, kPreThreads>(a, sh.part, first_unit);
-  const int64_t total = sh.part.total, u0 = first_unit(total), u1 = u0 + per < total ? u0 + per : total;
-  if (u0 >= u1) return;
-  WorkCursor<kPreRows, kUnitGranules> w;
-  w.start(a, sh.part.b, sh.part.tile, sh.part.base, u0);
+  const int64_t total = sh.part.total, u0 = first_unit(total);
+  if (u0 >= total) return;
+  WorkCursor<kPreRows, kUnitGranules>& w = sh.cursor[warp];
+  if (lane == 0) w.start(a, sh.part.b, sh.part.tile, sh.part.base, u0);
+  if (tid == 0) {
+    sh.u1 = u0 + per < total ? u0 + per : total;
+    sh.per = per;
+  }
   fence_proxy_async_smem();
   if (warp == 12) {
     tmem_alloc(&sh.tmem, 512);
@@ -218,17 +272,35 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   auto timed_out = [&]() {
     if (lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
   };
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, &sh.abort, kAttnWaitNs); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    uint32_t spins = 0;
+    const int64_t t0 = clock64();
+    while (true) {
+      const bool done = mbar_try_wait(bar, parity);
+      if (__all_sync(0xFFFFFFFFu, done)) return true;
+      if ((++spins & 15u) == 0 && __any_sync(0xFFFFFFFFu, sh.abort || clock64() - t0 > kAttnWaitCycles)) {
+        sh.abort = 1;
+        return false;
+      }
+    }
+  };
   // place of K (2t) or V (2t + 1) in the ring of tiles, and the parity of its turn there
   auto place = [](uint32_t x) { return x % Sh::kTiles; };
   auto turn_of = [](uint32_t x) { return (x / Sh::kTiles) & 1; };
-  // unit range of this CTA within the work
-  auto from_unit = [&](int64_t u) { return (int)(u - w.w0); };
-  auto to_unit = [&]() { return (int)(u1 - w.w0 < w.n ? u1 - w.w0 : (int64_t)w.n); };
+  // units of the work that are this CTA's: its part begins at u0 and at the first unit of every later work
+  // (the reductions make the values warp-uniform to the compiler as well)
+  auto from_unit = [&]() { return uniform((int)(w.w0 < u0 ? u0 - w.w0 : 0)); };
+  auto to_unit = [&]() { return uniform((int)(sh.u1 - w.w0 < w.n ? sh.u1 - w.w0 : (int64_t)w.n)); };
+  auto next_work = [&]() {  // the warp's cursor moves on; false at the end of the part
+    __syncwarp();
+    int more = 0;
+    if (lane == 0) more = w.w0 + w.n < sh.u1 && w.next(a);
+    __syncwarp();
+    return __any_sync(0xFFFFFFFFu, more) != 0;
+  };
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax
-    regs_inc<152>();  // 2 * 152 + 104 + 104 = 4 * 128, what the block was launched with
     const int i = warp >> 2, wq = warp & 3, row = tid & 127;
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
     const uint32_t t_s = tmem + lane_base + i * 128, t_o = tmem + lane_base + 256 + i * D;
@@ -241,9 +313,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       return wait(&sh.group[i], meets++ & 1);
     };
     bool ok = true;
-    for (int64_t u = u0; ok;) {
-      const int j0 = from_unit(u), j1 = to_unit();
-      u = w.w0 + j1;
+    while (ok) {
+      const int j0 = from_unit(), j1 = to_unit();
       const int32_t nrows = w.seq.rows * a.group;
       const int32_t r0 = w.tile * kPreRows + i * 128, r = r0 + row;
       if (r0 < nrows) {
@@ -283,23 +354,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         const Visible last_row = visible(pos0 + r_last / a.group, w.seq.len, a.causal, a.window);
         Visible mine = visible(pos0 + r / a.group, w.seq.len, a.causal, a.window);
         if (!live) mine = Visible{0, 0x7FFFFFFF};  // never written
-        const int32_t all_lo = last_row.lo, all_hi = first_row.hi;
+        // lanes 0..7: the page of granule 8j + lane (0 behind the span), looked at one tile later
         const int32_t* table = a.ix.table + (int64_t)w.b * a.ix.width;
         const int32_t gend = w.span.g0 + w.span.n;
-        // lanes 0..7: whether the page of granule g0 + 8j + lane is none
-        auto no_page = [&](int j) {
-          const int gi = w.span.g0 + kUnitGranules * j + (lane & 7);
-          const int32_t p = gi < gend ? table[gi / gpp] : 0;
-          return p < 0 || p >= a.ix.num_pages;
-        };
-        bool bad_next = w.span.n > 0 && no_page(j0);
+        int32_t gi = w.span.g0 + kUnitGranules * j0 + (lane & 7);
+        int32_t page = gi < gend ? table[gi >> a.ix.gshift] : 0;
+        int32_t tok0 = (w.span.g0 + kUnitGranules * j0) * kGranule;
+        const int32_t all_lo = last_row.lo, all_hi = w.span.n > 0 ? first_row.hi : 0;
 
         float m = kStartMax, l = 0.0f;
-        for (int j = j0; j < j1; ++j) {
-          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, bad_next);
-          if (j + 1 < j1) bad_next = no_page(j + 1);
-          const int32_t tok0 = (w.span.g0 + kUnitGranules * j) * kGranule;
-          const bool whole = w.span.n > 0 && tok0 >= all_lo && tok0 + kTileTokens <= all_hi && bad == 0;
+        for (int j = j0; j < j1; ++j, tok0 += kTileTokens) {
+          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, page < 0 || page >= a.ix.num_pages);
+          gi += kUnitGranules;
+          page = gi < gend ? table[gi >> a.ix.gshift] : 0;
+          const bool whole = tok0 >= all_lo && tok0 + kTileTokens <= all_hi && bad == 0;
           if (!(ok = wait(&sh.s_full[i], tiles & 1))) break;
           tc_fence_after();
           if (!whole) {  // what a row does not see becomes -Inf in place
@@ -434,7 +502,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           }
           __threadfence();
           if (!(ok = meet())) break;
-          const int64_t c0 = w.w0 / per, c1 = (w.w0 + w.n - 1) / per;
+          const int64_t c0 = w.w0 / sh.per, c1 = (w.w0 + w.n - 1) / sh.per;
           if (row == 0) {
             const int last = atomicAdd(&a.counters[2 * c0 + i], 1) == (int)(c1 - c0);
             if (last) a.counters[2 * c0 + i] = 0;
@@ -476,19 +544,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         }
         tc_fence_before();
       }
-      if (u >= u1 || !w.next(a)) break;
+      if (!next_work()) break;
     }
     if (!ok) timed_out();
   } else if (warp < 12) {
     // ------------------------------------------------------ dequantization
-    regs_dec<104>();
     const int dw = warp - 8;
     uint32_t phase = 0, it = 0;   // ring parities; K/V tiles done
     uint32_t in_flight = 0;       // ring stages with a copy that was not waited for
     bool ok = true;
-    for (int64_t u = u0; ok;) {
-      const int j0 = from_unit(u), j1 = to_unit();
-      u = w.w0 + j1;
+    while (ok) {
+      const int j0 = from_unit(), j1 = to_unit();
       const int cnt = 2 * (j1 - j0);  // this warp's granules: 8*tile + dw and + 4
       const int32_t* table = a.ix.table + (int64_t)w.b * a.ix.width;
       auto granule = [&](int x) { return kUnitGranules * (j0 + (x >> 1)) + dw + 4 * (x & 1); };  // within the span
@@ -496,7 +562,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         const int x = x0 + lane;
         int32_t p = -1;
         if (x < cnt && granule(x) < w.span.n) {
-          const int pi = (w.span.g0 + granule(x)) / gpp;
+          const int pi = (w.span.g0 + granule(x)) >> a.ix.gshift;
           if (NVFP4_IN_BOUNDS(pi, a.ix.width, a.status)) p = table[pi];
           if (p < 0 || p >= a.ix.num_pages) {
             record_status(a.status, NVFP4_ERR_PAGE);
@@ -508,11 +574,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       int32_t ids = -1, next_ids = -1;
       auto issue = [&](int x) {
         if ((x & 31) == 0) next_ids = fetch_ids(x);
-        const int32_t p = __shfl_sync(0xFFFFFFFFu, next_ids, x & 31);
+        const int32_t p = uniform(__shfl_sync(0xFFFFFFFFu, next_ids, x & 31));
         if (p < 0) return;
         const int gi = w.span.g0 + granule(x), st = x % kRing;
-        int64_t at = (((int64_t)p * a.ix.hkv + w.head) * gpp + gi % gpp) * kGB;
-        if (!NVFP4_IN_BOUNDS(at + kGB - 1, a.ix.num_pages * a.ix.hkv * gpp * kGB, a.status)) at = 0;
+        int64_t at = ((((int64_t)p * a.ix.hkv + w.head) << a.ix.gshift) + (gi & ((1 << a.ix.gshift) - 1))) * kGB;
+        if (!NVFP4_IN_BOUNDS(at + kGB - 1, (a.ix.num_pages * a.ix.hkv << a.ix.gshift) * kGB, a.status)) at = 0;
         if (lane == 0) {
           mbar_arrive_expect_tx(&sh.ring_full[dw][st], kGB);
           bulk_load(sh.ring[dw][st], a.pages + at, kGB, &sh.ring_full[dw][st]);
@@ -548,7 +614,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         bool some[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          some[y] = __shfl_sync(0xFFFFFFFFu, ids, (x + y) & 31) >= 0;
+          some[y] = (__ballot_sync(0xFFFFFFFFu, ids >= 0) >> ((x + y) & 31)) & 1u;
           if (some[y] && ok) {
             const int rs = (x + y) % kRing;
             ok = wait(&sh.ring_full[dw][rs], (phase >> rs) & 1u);
@@ -572,7 +638,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           if (x + y + kRing < cnt) issue(x + y + kRing);
         ++it;
       }
-      if (!ok || u >= u1 || !w.next(a)) break;
+      if (!ok || !next_work()) break;
     }
     if (!ok) {
       timed_out();
@@ -586,7 +652,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     }
   } else {
     // ----------------------------------------------------------- MMA issue
-    regs_dec<104>();
     if (warp < 14) {
       const int i = warp - 12;
       constexpr uint32_t idesc_s = idesc_f16(kTileTokens, false), idesc_o = idesc_f16(D, true);
@@ -598,18 +663,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         if (!wait(&sh.full[st], turn_of(2 * t))) return false;
         tc_fence_after();
         const uint64_t qd = smem_desc(smem_u32(sh.q[i]), 16, 1024, 2), kd = smem_desc(smem_u32(sh.kv[st]), 16, 1024, 2);
-#pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk) {  // 32 bytes within a 64-dimension half, halves 16 KB apart
-          const uint64_t off = (uint64_t)((kk & 3) * 2 + (kk >> 2) * (kTileTokens * 128 / 16));
-          mma_f16_ss_elect(t_s, qd + off, kd + off, idesc_s, kk != 0);
-        }
-        tc_commit_elect(&sh.s_full[i]);
-        tc_commit_elect(&sh.empty[st]);
+        mma_scores<D>(t_s, qd, kd, idesc_s, &sh.s_full[i], &sh.empty[st]);
         return true;
       };
-      for (int64_t u = u0; ok;) {
-        const int j0 = from_unit(u), j1 = to_unit();
-        u = w.w0 + j1;
+      while (ok) {
+        const int j0 = from_unit(), j1 = to_unit();
         const int n = j1 - j0;
         if (w.tile * kPreRows + i * 128 < w.seq.rows * a.group) {
           if (!(ok = wait(&sh.q_full[i], works & 1))) break;
@@ -624,15 +682,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
             for (int half = 0; half < 2; ++half) {
               if (!(ok = wait(half ? &sh.p_full[i] : &sh.p_low[i], tiles & 1))) break;
               tc_fence_after();
-#pragma unroll
-              for (int k4 = 0; k4 < 4; ++k4) {  // 16 tokens: two groups of eight rows of 128 bytes
-                const int kk = 4 * half + k4;
-                mma_f16_ts_elect(t_o, t_s + 8 * kk, vd + (uint64_t)(kk * 2048 / 16), idesc_o, (j | kk) != 0);
-              }
+              mma_values(t_o, t_s + 32 * half, vd + (uint64_t)(half * 4 * 2048 / 16), idesc_o, (j | half) != 0);
             }
             if (!ok) break;
-            tc_commit_elect(&sh.pv_done[i]);
-            tc_commit_elect(&sh.empty[st]);
+            commit_two(&sh.pv_done[i], &sh.empty[st]);
             if (!(ok = wait(&sh.pv_done[i], tiles & 1))) break;
             if (j + 1 < n && !(ok = scores(it + 1))) break;
           }
@@ -645,7 +698,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
             __syncwarp();
           }
         }
-        if (!ok || u >= u1 || !w.next(a)) break;
+        if (!ok || !next_work()) break;
       }
       if (!ok) {
         timed_out();
