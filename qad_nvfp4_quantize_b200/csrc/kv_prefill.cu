@@ -7,26 +7,27 @@
 //
 // One CTA per SM walks its part of the work list; a work is 256 query rows (two
 // tiles of 128) of one KV head against its cached tokens, 128 at a time.
-//   warps 0..3, 4..7   softmax of row tile 0 and 1, a thread per row: scores
-//                      from tensor memory, p = 2^(s*c - m) as FP16 pairs back
-//                      into the same columns, the output's rescaling and the
-//                      epilogue;
+//   warps 0..3, 4..7   softmax of row tile 0 and 1, a thread per row, in steps
+//                      of 64 tokens: scores from tensor memory, p = 2^(s*c - m)
+//                      as FP16 pairs back into the same columns, the output's
+//                      rescaling and the epilogue;
 //   warps 8..11        dequantization: each keeps bulk copies of its granules
 //                      in flight (ring of kRing) and writes K and V as FP16
 //                      rows of 64 dimensions, 128-byte swizzled, into a ring
 //                      of three tiles (K0 V0 K1 V1 ...);
 //   warps 12, 13       issue the MMAs of row tile 0 and 1: S = Q K^T (K-major
-//                      operands), O += P V (P from tensor memory, V read with
-//                      its 64-dimension runs as the MN-major operand).
-// Two row tiles take turns: while one is in softmax the tensor pipe works for
-// the other, and each dequantized tile serves 256 rows. Tensor memory: S/P 128
-// columns and O D columns per row tile. S of the next tile is issued once P V
-// of this one is complete (its columns hold P), which also means that O is at
-// rest whenever a softmax warp has scores to look at: it rescales O by itself.
+//                      operands), O += P V (P from tensor memory, V with its
+//                      64-dimension runs as the MN-major operand).
+// Tensor memory, for each row tile: two S/P buffers of 64 columns and O of D.
+// While the softmax works on step t, S of step t + 1 is there already; S of
+// step t + 2 is issued when P V of step t is complete (its columns hold P).
+// What this buys: with one S of 128 tokens per row tile the softmax waited for
+// P V and the next S each time (4,096 over 12,288: 741 us). Two row tiles, not
+// one, because each dequantized tile then serves 256 rows.
 //
 // The running maximum m is allowed to lag by 8 (in log2 units): a row takes a
 // new one, and O is rescaled, only when a score exceeds it by more, so that p
-// stays below 2^8 and most tiles leave O alone.
+// stays below 2^8 and most steps leave O alone.
 #include <cuda_fp16.h>
 
 #include "kv_attention.cuh"
@@ -52,7 +53,7 @@ struct PreShared {
   uint8_t ring[4][kRing][granule_bytes(D)];
   uint64_t ring_full[4][kRing];
   uint64_t full[kTiles], empty[kTiles];
-  uint64_t q_full[2], s_full[2], p_low[2], p_full[2], pv_done[2], turn[2], group[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], group[2];
   WorkCursor<kPreRows, kUnitGranules> cursor[kPreThreads / 32];  // one per warp: no register is spent on it
   int64_t u1, per;
   uint32_t tmem;
@@ -64,55 +65,49 @@ struct PreShared {
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-// A run of MMAs and the commits behind it, issued by one elected lane of a
-// converged warp: one statement, because electing and setting up each
-// instruction by itself took the issuing warp 70 cycles, longer than the tensor
-// pipe needs for it.
+// A run of MMAs issued by one elected lane of a converged warp: one statement,
+// so that the lane is elected once.
 // S[tmem] = Q K^T over D dimensions: 32 bytes a step within a 64-dimension
-// half, halves 16 KB (1024 descriptor units) apart. Then arrives on both
-// barriers when all of the thread's MMAs are complete.
+// half, halves 16 KB (1024 descriptor units) apart.
 template <int D>
-NVFP4_DEVINL void mma_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc, uint64_t* bar0, uint64_t* bar1) {
-  if constexpr (D == 128)
+NVFP4_DEVINL void mma_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
+  if constexpr (D == 128) {
     asm volatile(
-      "{\n\t.reg .pred e, t, z;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 z, 0, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\t"
-      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
-      "}"
-      ::"r"(d), "l"(q), "l"(k), "r"(idesc), "r"(smem_u32(bar0)), "r"(smem_u32(bar1))
-      : "memory");
-  else
+        "{\n\t.reg .pred e, t, z;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 z, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "}"
+        ::"r"(d), "l"(q), "l"(k), "r"(idesc)
+        : "memory");
+  } else {
     asm volatile(
-      "{\n\t.reg .pred e, t, z;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 z, 0, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\t"
-      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
-      "}"
-      ::"r"(d), "l"(q), "l"(k), "r"(idesc), "r"(smem_u32(bar0)), "r"(smem_u32(bar1))
-      : "memory");
+        "{\n\t.reg .pred e, t, z;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 z, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "}"
+        ::"r"(d), "l"(q), "l"(k), "r"(idesc)
+        : "memory");
+  }
 }
 // O[tmem] (+)= P V of 64 tokens: P in 8 columns a step, V in two groups of
 // eight rows of 128 bytes.
@@ -129,16 +124,6 @@ NVFP4_DEVINL void mma_values(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc,
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t"
       "}"
       ::"r"(d), "r"(p), "l"(v), "r"(idesc), "r"(acc)
-      : "memory");
-}
-NVFP4_DEVINL void commit_two(uint64_t* bar0, uint64_t* bar1) {
-  asm volatile(
-      "{\n\t.reg .pred e, t, z;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t"
-      "}"
-      ::"r"(smem_u32(bar0)), "r"(smem_u32(bar1))
       : "memory");
 }
 // Columns of this warp's 32 tensor-memory lanes, with the wait: one statement,
@@ -236,11 +221,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 4);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_low[i], 4);
-      mbar_init(&sh.p_full[i], 4);
-      mbar_init(&sh.pv_done[i], 1);
-      mbar_init(&sh.turn[i], 4);
+      mbar_init(&sh.s_full[i][0], 1);
+      mbar_init(&sh.s_full[i][1], 1);
+      mbar_init(&sh.p_full[i][0], 4);
+      mbar_init(&sh.p_full[i][1], 4);
+      mbar_init(&sh.pv_done[i][0], 1);
+      mbar_init(&sh.pv_done[i][1], 1);
       mbar_init(&sh.group[i], 4);
     }
     sh.abort = 0;
@@ -272,7 +258,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   auto timed_out = [&]() {
     if (lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
   };
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
+  auto wait = [&](uint64_t* bar, uint32_t parity) {  // by the whole warp; a completed phase costs one poll
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
     uint32_t spins = 0;
     const int64_t t0 = clock64();
     while (true) {
@@ -305,8 +292,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
     const uint32_t t_s = tmem + lane_base + i * 128, t_o = tmem + lane_base + 256 + i * D;
     const float kg = *a.k_g, vg = *a.v_g;
-    uint32_t tiles = 0;  // tiles done by this row tile
-    uint32_t meets = 0, turns = 0;
+    uint32_t steps = 0, meets = 0;
     auto meet = [&]() {  // the four warps of the row tile, with the usual bound
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.group[i]);
@@ -344,7 +330,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full[i]);
 
-        const bool both = w.tile * kPreRows + 128 < nrows;  // the other row tile has rows too
         // ---- limits of this row and of the row tile
         // not zero: a masked score is -Inf before it is multiplied
         const float factor = fmaxf(scale_exp2(a.scale * kg * kLog2e, kValueExp - ex), 1.17549435e-38f);
@@ -354,59 +339,58 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         const Visible last_row = visible(pos0 + r_last / a.group, w.seq.len, a.causal, a.window);
         Visible mine = visible(pos0 + r / a.group, w.seq.len, a.causal, a.window);
         if (!live) mine = Visible{0, 0x7FFFFFFF};  // never written
-        // lanes 0..7: the page of granule 8j + lane (0 behind the span), looked at one tile later
+        // lanes 0..3: the pages of the next step's granules (0 behind the span), looked at one step later
         const int32_t* table = a.ix.table + (int64_t)w.b * a.ix.width;
         const int32_t gend = w.span.g0 + w.span.n;
-        int32_t gi = w.span.g0 + kUnitGranules * j0 + (lane & 7);
+        int32_t gi = w.span.g0 + kUnitGranules * j0 + (lane & 3);
         int32_t page = gi < gend ? table[gi >> a.ix.gshift] : 0;
         int32_t tok0 = (w.span.g0 + kUnitGranules * j0) * kGranule;
         const int32_t all_lo = last_row.lo, all_hi = w.span.n > 0 ? first_row.hi : 0;
 
         float m = kStartMax, l = 0.0f;
-        for (int j = j0; j < j1; ++j, tok0 += kTileTokens) {
+        for (int x = 2 * (j1 - j0); x > 0; --x, ++steps, tok0 += 64) {
           const uint32_t bad = __ballot_sync(0xFFFFFFFFu, page < 0 || page >= a.ix.num_pages);
-          gi += kUnitGranules;
+          gi += 4;
           page = gi < gend ? table[gi >> a.ix.gshift] : 0;
-          const bool whole = tok0 >= all_lo && tok0 + kTileTokens <= all_hi && bad == 0;
-          if (!(ok = wait(&sh.s_full[i], tiles & 1))) break;
+          const bool whole = tok0 >= all_lo && tok0 + 64 <= all_hi && bad == 0;
+          const uint32_t t_x = t_s + 64 * (steps & 1);
+          if (!(ok = wait(&sh.s_full[i][steps & 1], (steps >> 1) & 1))) break;
           tc_fence_after();
           if (!whole) {  // what a row does not see becomes -Inf in place
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t x[16];
-              tmem_read16(t_s + 16 * c, x);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t y[16];
+              tmem_read16(t_x + 16 * c, y);
               const int32_t t0 = tok0 + 16 * c;
               const bool none = (bad >> c) & 1u;
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (none || t0 + e < mine.lo || t0 + e >= mine.hi) x[e] = 0xFF800000u;
-              tmem_st16(t_s + 16 * c, x);
+                if (none || t0 + e < mine.lo || t0 + e >= mine.hi) y[e] = 0xFF800000u;
+              tmem_st16(t_x + 16 * c, y);
             }
             tmem_wait_st();
           }
-          // the row's maximum: columns 64..127 are read again below, 0..63 stay in registers
-          uint32_t x[64];
-          auto largest = [&]() {
-            float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
+          uint32_t y[64];
+          tmem_read64(t_x, y);
+          float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
 #pragma unroll
-            for (int e = 0; e < 64; e += 8) {
-              t0 = max3(t0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-              t1 = max3(t1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-              t2 = max3(t2, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
-              t3 = max3(t3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
-            }
-            return max3(fmaxf(t0, t1), t2, t3);
-          };
-          tmem_read64(t_s + 64, x);
-          float top = largest();
-          tmem_read64(t_s, x);
-          top = fmaxf(top, largest()) * factor;
+          for (int e = 0; e < 64; e += 8) {
+            t0 = max3(t0, __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+            t1 = max3(t1, __uint_as_float(y[e + 2]), __uint_as_float(y[e + 3]));
+            t2 = max3(t2, __uint_as_float(y[e + 4]), __uint_as_float(y[e + 5]));
+            t3 = max3(t3, __uint_as_float(y[e + 6]), __uint_as_float(y[e + 7]));
+          }
+          const float top = max3(fmaxf(t0, t1), t2, t3) * factor;
           if (__any_sync(0xFFFFFFFFu, top > m + kRescaleAt)) {
             const float m1 = fmaxf(m, top);
             const float f = m == kStartMax ? 0.0f : ex2(m - m1);
             m = m1;
             l *= f;
-            if (j > j0) {
+            if (x < 2 * (j1 - j0)) {
+              // O at rest. (The buffer's earlier P V is known to be complete, or its S could not have come: the parity is
+              // not ambiguous.)
+              if (!(ok = wait(&sh.pv_done[i][(steps - 1) & 1], ((steps - 1) >> 1) & 1))) break;
+              tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
@@ -417,50 +401,38 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
               }
             }
           }
-          // p of 64 columns as FP16 pairs into 32 columns whose scores have been read
+          // p as FP16 pairs (to 2^-11 of itself) into the first half of the buffer
           f32x2 sum = 0;
           const f32x2 ff = pack2(factor, factor), mm = pack2(-m, -m);
-          auto weights = [&](uint32_t to, uint64_t* bar) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t p[16];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float a0, a1;
-                unpack2(fma2(pack2(__uint_as_float(x[32 * c + 2 * e]), __uint_as_float(x[32 * c + 2 * e + 1])), ff, mm),
-                        a0, a1);
-                a0 = ex2(a0);
-                a1 = ex2(a1);
-                sum = add2(sum, pack2(a0, a1));
-                p[e] = half2_of(a0, a1);
-              }
-              tmem_st16(to + 16 * c, p);
+            for (int e = 0; e < 16; ++e) {
+              float a0, a1;
+              unpack2(fma2(pack2(__uint_as_float(y[32 * c + 2 * e]), __uint_as_float(y[32 * c + 2 * e + 1])), ff, mm), a0,
+                      a1);
+              a0 = ex2(a0);
+              a1 = ex2(a1);
+              sum = add2(sum, pack2(a0, a1));
+              p[e] = half2_of(a0, a1);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
-          };
-          // the two row tiles take turns at the 2^x unit: while one computes weights the tensor pipe has the other
-          if (both && !(ok = wait(&sh.turn[i], (turns & 1) ^ (i == 0 ? 1 : 0)))) break;
-          weights(t_s, &sh.p_low[i]);
-          tmem_read64(t_s + 64, x);
-          weights(t_s + 32, &sh.p_full[i]);
-          if (both) {
-            if (lane == 0) mbar_arrive(&sh.turn[1 - i]);
-            ++turns;
+            tmem_st16(t_x + 16 * c, p);
           }
           {
             float s0, s1;
             unpack2(sum, s0, s1);
             l += s0 + s1;
           }
-          ++tiles;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_full[i][steps & 1]);
         }
         if (!ok) break;
 
-        // ---- epilogue: O of the last tile is complete
-        if (!(ok = wait(&sh.pv_done[i], (tiles - 1) & 1))) break;
+        // ---- epilogue: O of the last step is complete
+        if (!(ok = wait(&sh.pv_done[i][(steps - 1) & 1], ((steps - 1) >> 1) & 1))) break;
         tc_fence_after();
         const bool whole_work = j0 == 0 && j1 == w.n;
         const int64_t at = tok * a.ix.hkv * a.group + hq;
@@ -654,16 +626,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     // ----------------------------------------------------------- MMA issue
     if (warp < 14) {
       const int i = warp - 12;
-      constexpr uint32_t idesc_s = idesc_f16(kTileTokens, false), idesc_o = idesc_f16(D, true);
+      constexpr uint32_t idesc_s = idesc_f16(64, false), idesc_o = idesc_f16(D, true);
       const uint32_t t_s = tmem + i * 128, t_o = tmem + 256 + i * D;
-      uint32_t it = 0, tiles = 0, works = 0;
+      uint32_t it = 0, steps = 0, works = 0;
       bool ok = true;
-      auto scores = [&](uint32_t t) {  // S = Q K^T of K/V tile t
+      const uint64_t qd = smem_desc(smem_u32(sh.q[i]), 16, 1024, 2);
+      auto scores = [&](uint32_t t, uint32_t half) {  // S = Q K^T of 64 tokens (64 rows of 128 bytes) of tile t
         const uint32_t st = place(2 * t);
-        if (!wait(&sh.full[st], turn_of(2 * t))) return false;
-        tc_fence_after();
-        const uint64_t qd = smem_desc(smem_u32(sh.q[i]), 16, 1024, 2), kd = smem_desc(smem_u32(sh.kv[st]), 16, 1024, 2);
-        mma_scores<D>(t_s, qd, kd, idesc_s, &sh.s_full[i], &sh.empty[st]);
+        if (half == 0) {
+          if (!wait(&sh.full[st], turn_of(2 * t))) return false;
+          tc_fence_after();
+        }
+        mma_scores<D>(t_s + 64 * half, qd, smem_desc(smem_u32(sh.kv[st]), 16, 1024, 2) + half * 512, idesc_s);
+        tc_commit_elect(&sh.s_full[i][half]);
+        if (half) tc_commit_elect(&sh.empty[st]);
         return true;
       };
       while (ok) {
@@ -673,21 +649,22 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           if (!(ok = wait(&sh.q_full[i], works & 1))) break;
           ++works;
           tc_fence_after();
-          if (!(ok = scores(it))) break;
-          for (int j = 0; j < n; ++j, ++it, ++tiles) {
+          if (!(ok = scores(it, 0) && scores(it, 1))) break;
+          for (int j = 0; j < n; ++j, ++it) {
             const uint32_t st = place(2 * it + 1);
             if (!(ok = wait(&sh.full[st], turn_of(2 * it + 1)))) break;
             const uint64_t vd = smem_desc(smem_u32(sh.kv[st]), kTileTokens * 128, 1024, 2);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (!(ok = wait(half ? &sh.p_full[i] : &sh.p_low[i], tiles & 1))) break;
+            for (uint32_t half = 0; half < 2; ++half, ++steps) {
+              if (!(ok = wait(&sh.p_full[i][half], (steps >> 1) & 1))) break;
               tc_fence_after();
-              mma_values(t_o, t_s + 32 * half, vd + (uint64_t)(half * 4 * 2048 / 16), idesc_o, (j | half) != 0);
+              mma_values(t_o, t_s + 64 * half, vd + half * (4 * 2048 / 16), idesc_o, (j | (int)half) != 0);
+              tc_commit_elect(&sh.pv_done[i][half]);
+              if (half) tc_commit_elect(&sh.empty[st]);
+              if (!(ok = wait(&sh.pv_done[i][half], (steps >> 1) & 1))) break;
+              if (j + 1 < n && !(ok = scores(it + 1, half))) break;
             }
             if (!ok) break;
-            commit_two(&sh.pv_done[i], &sh.empty[st]);
-            if (!(ok = wait(&sh.pv_done[i], tiles & 1))) break;
-            if (j + 1 < n && !(ok = scores(it + 1))) break;
           }
         } else {  // no rows in this half: the stages are only passed on
           for (int j = 0; j < n && ok; ++j, ++it) {
