@@ -11,10 +11,10 @@
 //                      of 64 tokens: scores from tensor memory, p = 2^(s*c - m)
 //                      as FP16 pairs back into the same columns, the output's
 //                      rescaling and the epilogue;
-//   warps 8..11        dequantization: each keeps bulk copies of its granules
-//                      in flight (ring of kRing) and writes K and V as FP16
-//                      rows of 64 dimensions, 128-byte swizzled, into a ring
-//                      of three tiles (K0 V0 K1 V1 ...);
+//   warp 14            bulk copies of the codes, kStages tiles ahead;
+//   warps 8..11        dequantization: K and V as FP16 rows of 64 dimensions,
+//                      128-byte swizzled, into a ring of three tiles (K0 V0 K1
+//                      V1 ...);
 //   warps 12, 13       issue the MMAs of row tile 0 and 1: S = Q K^T (K-major
 //                      operands), O += P V (P from tensor memory, V with its
 //                      64-dimension runs as the MN-major operand).
@@ -42,7 +42,7 @@ constexpr float kStartMax = -1e30f;  // m before the first visible token, in log
 
 template <int D>
 struct PreShared {
-  static constexpr int kRing = 7;
+  static constexpr int kStages = 3;  // tiles of codes in flight
   static constexpr int kTiles = 3;
   static constexpr int kTile = kTileTokens * D * 2;  // bytes of an FP16 tile
   uint8_t kv[kTiles][kTile];                         // K and V tiles in turn: K0 V0 K1 V1 ...
@@ -50,8 +50,9 @@ struct PreShared {
     uint8_t q[2][kTile];
     PartShared part;
   };
-  uint8_t ring[4][kRing][granule_bytes(D)];
-  uint64_t ring_full[4][kRing];
+  uint8_t codes[kStages][kUnitGranules][granule_bytes(D)];
+  uint64_t codes_full[kStages], codes_empty[kStages];
+  uint32_t there[kStages];  // bit g: granule g of the tile is there (within the span, on a page of the pool)
   uint64_t full[kTiles], empty[kTiles];
   uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], group[2];
   WorkCursor<kPreRows, kUnitGranules> cursor[kPreThreads / 32];  // one per warp: no register is spent on it
@@ -207,14 +208,16 @@ NVFP4_DEVINL uint32_t tile_chunk(int h, int r, int c) {
 template <int D>
 __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnArgs a) {
   using Sh = PreShared<D>;
-  constexpr int kGB = granule_bytes(D), kRing = Sh::kRing;
+  constexpr int kGB = granule_bytes(D), kStages = Sh::kStages;
   extern __shared__ uint8_t pre_smem[];
   Sh& sh = *reinterpret_cast<Sh*>((reinterpret_cast<uintptr_t>(pre_smem) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
 
   if (tid == 0) {
-    for (int w = 0; w < 4; ++w)
-      for (int i = 0; i < kRing; ++i) mbar_init(&sh.ring_full[w][i], 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.codes_full[i], 1);
+      mbar_init(&sh.codes_empty[i], 4);
+    }
     for (int i = 0; i < Sh::kTiles; ++i) {
       mbar_init(&sh.full[i], 4);
       mbar_init(&sh.empty[i], 2);
@@ -522,104 +525,101 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   } else if (warp < 12) {
     // ------------------------------------------------------ dequantization
     const int dw = warp - 8;
-    uint32_t phase = 0, it = 0;   // ring parities; K/V tiles done
-    uint32_t in_flight = 0;       // ring stages with a copy that was not waited for
+    uint32_t it = 0;  // K/V tiles done
     bool ok = true;
     while (ok) {
-      const int j0 = from_unit(), j1 = to_unit();
-      const int cnt = 2 * (j1 - j0);  // this warp's granules: 8*tile + dw and + 4
-      const int32_t* table = a.ix.table + (int64_t)w.b * a.ix.width;
-      auto granule = [&](int x) { return kUnitGranules * (j0 + (x >> 1)) + dw + 4 * (x & 1); };  // within the span
-      auto fetch_ids = [&](int x0) {
-        const int x = x0 + lane;
-        int32_t p = -1;
-        if (x < cnt && granule(x) < w.span.n) {
-          const int pi = (w.span.g0 + granule(x)) >> a.ix.gshift;
-          if (NVFP4_IN_BOUNDS(pi, a.ix.width, a.status)) p = table[pi];
-          if (p < 0 || p >= a.ix.num_pages) {
-            record_status(a.status, NVFP4_ERR_PAGE);
-            p = -1;
-          }
-        }
-        return p;
-      };
-      int32_t ids = -1, next_ids = -1;
-      auto issue = [&](int x) {
-        if ((x & 31) == 0) next_ids = fetch_ids(x);
-        const int32_t p = uniform(__shfl_sync(0xFFFFFFFFu, next_ids, x & 31));
-        if (p < 0) return;
-        const int gi = w.span.g0 + granule(x), st = x % kRing;
-        int64_t at = ((((int64_t)p * a.ix.hkv + w.head) << a.ix.gshift) + (gi & ((1 << a.ix.gshift) - 1))) * kGB;
-        if (!NVFP4_IN_BOUNDS(at + kGB - 1, (a.ix.num_pages * a.ix.hkv << a.ix.gshift) * kGB, a.status)) at = 0;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sh.ring_full[dw][st], kGB);
-          bulk_load(sh.ring[dw][st], a.pages + at, kGB, &sh.ring_full[dw][st]);
-        }
-        in_flight |= 1u << st;
-      };
-      // K (which = 0) or V of granule x into rows 16*(its place in the tile) of an FP16 tile; zeros for none
-      auto expand = [&](int x, bool some, int which, uint8_t* tile) {
-        const uint8_t* gr = sh.ring[dw][x % kRing] + which * 9 * D;
-        const int r = (granule(x) % kUnitGranules) * kGranule + (lane >> 1);
+      for (int x = to_unit() - from_unit(); x > 0; --x, ++it) {
+        const uint32_t st = it % kStages;
+        if (!(ok = wait(&sh.codes_full[st], (it / kStages) & 1))) break;
+        const uint32_t there = uniform((int)sh.there[st]);
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {  // two lanes share the 64 dimensions of half h of a token
-          uint4 codes = make_uint4(0, 0, 0, 0);
-          uint32_t sc = 0;
-          if (some) {
-            codes = *reinterpret_cast<const uint4*>(gr + (lane >> 1) * (D / 2) + h * 32 + (lane & 1) * 16);
-            sc = *reinterpret_cast<const uint16_t*>(gr + 8 * D + (lane >> 1) * (D / 16) + h * 4 + (lane & 1) * 2);
-          }
-          const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+        for (uint32_t which = 0; which < 2; ++which) {
+          // K or V of granules dw and dw + 4 into rows 16*dw.. and 64 + 16*dw.. of an FP16 tile, zeros for those that
+          // are not there; two lanes share the 64 dimensions of half h of a token. All loads come first: the stores
+          // may not be moved behind them, and each trip would wait for shared memory twice.
+          uint4 codes[2][D / 64];
+          uint32_t sc[2][D / 64];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t f = scales_to_half(__byte_perm(sc, 0, e < 2 ? 0x4040 : 0x4141));
-            uint32_t o[4];
-            codes_to_half(cw[e], o);
-            *reinterpret_cast<uint4*>(tile + tile_chunk(h, r, (lane & 1) * 4 + e)) =
-                make_uint4(hmul2(o[0], f), hmul2(o[1], f), hmul2(o[2], f), hmul2(o[3], f));
-          }
-        }
-      };
-      for (int x = 0; x < (cnt < kRing ? cnt : kRing); ++x) issue(x);
-      for (int x = 0; x < cnt; x += 2) {  // a tile: this warp's two granules
-        if ((x & 31) == 0) ids = fetch_ids(x);
-        bool some[2];
+          for (int y = 0; y < 2; ++y) {
+            const uint8_t* gr = sh.codes[st][dw + 4 * y] + which * 9 * D;
+            const bool some = (there >> (dw + 4 * y)) & 1u;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          some[y] = (__ballot_sync(0xFFFFFFFFu, ids >= 0) >> ((x + y) & 31)) & 1u;
-          if (some[y] && ok) {
-            const int rs = (x + y) % kRing;
-            ok = wait(&sh.ring_full[dw][rs], (phase >> rs) & 1u);
-            if (ok) {
-              phase ^= 1u << rs;
-              in_flight &= ~(1u << rs);
+            for (int h = 0; h < D / 64; ++h) {
+              codes[y][h] = make_uint4(0, 0, 0, 0);
+              sc[y][h] = 0;
+              if (some) {
+                codes[y][h] = *reinterpret_cast<const uint4*>(gr + (lane >> 1) * (D / 2) + h * 32 + (lane & 1) * 16);
+                sc[y][h] =
+                    *reinterpret_cast<const uint16_t*>(gr + 8 * D + (lane >> 1) * (D / 16) + h * 4 + (lane & 1) * 2);
+              }
             }
           }
-        }
-        for (uint32_t which = 0; ok && which < 2; ++which) {
           const uint32_t tile = 2 * it + which;
           if (!(ok = wait(&sh.empty[place(tile)], turn_of(tile) ^ 1))) break;
-          expand(x, some[0], which, sh.kv[place(tile)]);
-          expand(x + 1, some[1], which, sh.kv[place(tile)]);
+          uint8_t* to = sh.kv[place(tile)];
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+              const uint32_t cw[4] = {codes[y][h].x, codes[y][h].y, codes[y][h].z, codes[y][h].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t f = scales_to_half(__byte_perm(sc[y][h], 0, e < 2 ? 0x4040 : 0x4141));
+                uint32_t o[4];
+                codes_to_half(cw[e], o);
+                *reinterpret_cast<uint4*>(
+                    to + tile_chunk(h, (dw + 4 * y) * kGranule + (lane >> 1), (lane & 1) * 4 + e)) =
+                    make_uint4(hmul2(o[0], f), hmul2(o[1], f), hmul2(o[2], f), hmul2(o[3], f));
+              }
+            }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.full[place(tile)]);
         }
         if (!ok) break;
-        for (int y = 0; y < 2; ++y)
-          if (x + y + kRing < cnt) issue(x + y + kRing);
-        ++it;
+        if (lane == 0) mbar_arrive(&sh.codes_empty[st]);
+      }
+      if (!ok || !next_work()) break;
+    }
+    if (!ok) timed_out();
+  } else if (warp == 14) {
+    // ------------------------------------------- bulk copies of the codes
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok) {
+      const int j0 = from_unit(), n = to_unit() - j0;
+      const int32_t* table = a.ix.table + (int64_t)w.b * a.ix.width;
+      const int32_t gend = w.span.g0 + w.span.n;
+      const int64_t page_bytes = ((int64_t)a.ix.hkv << a.ix.gshift) * kGB;
+      const uint8_t* head = a.pages + ((int64_t)w.head << a.ix.gshift) * kGB;
+      int32_t gi = w.span.g0 + kUnitGranules * j0 + (lane & 7);  // lanes 0..7: a granule each
+      auto page_of = [&](int32_t g) {  // -2 behind the span
+        return g < gend && NVFP4_IN_BOUNDS(g >> a.ix.gshift, a.ix.width, a.status) ? table[g >> a.ix.gshift] : -2;
+      };
+      int32_t page = page_of(gi);
+      for (int x = 0; x < n; ++x, ++it, gi += kUnitGranules) {
+        const uint32_t st = it % kStages;
+        const int32_t next = page_of(gi + kUnitGranules);
+        const bool good = page >= 0 && page < a.ix.num_pages;
+        if (!good && page != -2) record_status(a.status, NVFP4_ERR_PAGE);
+        int64_t at = page * page_bytes + (int64_t)(gi & ((1 << a.ix.gshift) - 1)) * kGB;
+        if (good && !NVFP4_IN_BOUNDS(at + kGB - 1, a.ix.num_pages * page_bytes, a.status)) at = 0;
+        const uint32_t there = __ballot_sync(0xFFFFFFFFu, good) & 0xFFu;
+        if (!(ok = wait(&sh.codes_empty[st], ((it / kStages) & 1) ^ 1))) break;
+        if (lane == 0) {
+          sh.there[st] = there;
+          mbar_arrive_expect_tx(&sh.codes_full[st], (uint32_t)__popc(there) * kGB);
+        }
+        __syncwarp();
+        if (lane < 8 && good) bulk_load(sh.codes[st][lane], head + at, kGB, &sh.codes_full[st]);
+        page = next;
       }
       if (!ok || !next_work()) break;
     }
     if (!ok) {
       timed_out();
-      // copies in flight land before the CTA exits (bounded)
-      for (int rs = 0; rs < kRing; ++rs) {
-        if (!((in_flight >> rs) & 1u)) continue;
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(&sh.ring_full[dw][rs], (phase >> rs) & 1u) && globaltimer_ns() - t0 < 1000000ull) {
-        }
+      const uint64_t t0 = globaltimer_ns();  // copies in flight land before the CTA may exit
+      while (globaltimer_ns() - t0 < 1000000ull) {
       }
     }
   } else {
