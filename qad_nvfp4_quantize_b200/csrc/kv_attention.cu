@@ -37,18 +37,19 @@ constexpr int kAttnThreads = kAttnWarps * 32;
 
 template <int D, int NT>
 struct AttnShared {
-  static constexpr int kStages = 5;
+  static constexpr int kStages = 3;  // pairs of granules in flight for each warp
   static constexpr int kRows = 8 * NT;
   static constexpr int kPad = D + 8;  // row pitch of the joining buffer
   union {
-    uint8_t ring[kAttnWarps][kStages][granule_bytes(D)];
+    uint8_t ring[kAttnWarps][kStages][2 * granule_bytes(D)];
     float join[kAttnWarps][kRows][kPad];
     PartShared part;
   };
   uint64_t bar[kAttnWarps][kStages];
   float wm[kAttnWarps][kRows], wl[kAttnWarps][kRows];
   float m[kRows], l[kRows];
-  int last, abort;
+  int last;
+  volatile int abort;
 };
 
 NVFP4_DEVINL void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -82,8 +83,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
   constexpr int kRows = Sh::kRows, kStages = Sh::kStages, kGB = granule_bytes(D);
   constexpr int kSteps = D / 16;        // k-steps of S, m-tiles of O
   constexpr int kWords = D / 32;        // code words per lane and K row
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int gpp = a.ix.page / kGranule;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), g = lane >> 2, t = lane & 3;
 
   if (lane == 0)
     for (int i = 0; i < kStages; ++i) mbar_init(&sh.bar[warp][i], 1);
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
   fence_proxy_async_smem();
   __syncthreads();  // the search's scratch lies over the ring
   uint32_t phase = 0;  // parity bit of each stage of this warp's ring
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity, &sh.abort); };
   const float kg = *a.k_g, vg = *a.v_g;
 
   for (int64_t u = u0;;) {
@@ -175,75 +176,83 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
     }
 
-    // ---- this warp's granules j0 + warp + 8*i of the work
-    const int cnt = w.span.n > 0 && j1 - j0 > warp ? (j1 - j0 - warp + kAttnWarps - 1) / kAttnWarps : 0;
-    const int gfirst = w.span.g0 + j0 + warp;
+    // ---- this warp's pairs of granules j0 + 2*(warp + 8*i) and the next one
+    const int cnt = uniform(w.span.n > 0 && j1 - j0 > 2 * warp ? (j1 - j0 - 2 * warp + 2 * kAttnWarps - 1) / (2 * kAttnWarps) : 0);
+    const int gfirst = w.span.g0 + j0 + 2 * warp, gend = w.span.g0 + j1;
     const int32_t* table = a.ix.table + (int64_t)b * a.ix.width;
-    int32_t ids = -1;  // lane i: page of granule (i0 & ~31) + i, -1 beyond the span or for a page that is none
-    auto fetch_ids = [&](int i0) {
-      const int i = i0 + lane;
-      int32_t p = -1;
-      if (i < cnt && NVFP4_IN_BOUNDS((gfirst + kAttnWarps * i) / gpp, a.ix.width, a.status)) {
-        p = table[(gfirst + kAttnWarps * i) / gpp];
-        if (p < 0 || p >= a.ix.num_pages) {
-          record_status(a.status, NVFP4_ERR_PAGE);
-          p = -1;
-        }
+    const int64_t page_bytes = ((int64_t)a.ix.hkv << a.ix.gshift) * kGB;
+    const uint8_t* of_head = a.pages + ((int64_t)head << a.ix.gshift) * kGB;
+    // Lane x of a block of 16 pairs looks after granule x & 1 of pair x >> 1: where it lies, and whether it is there
+    // (within the span, on a page of the pool; else its tokens count as masked).
+    const uint8_t* from = nullptr;
+    uint32_t there = 0, there_next = 0;
+    auto look_up = [&](int i0) {
+      const int i = i0 + (lane >> 1), gi = gfirst + 2 * kAttnWarps * i + (lane & 1);
+      bool good = i < cnt && gi < gend && NVFP4_IN_BOUNDS(gi >> a.ix.gshift, a.ix.width, a.status);
+      if (good) {
+        const int32_t p = table[gi >> a.ix.gshift];
+        good = p >= 0 && p < a.ix.num_pages;
+        if (!good) record_status(a.status, NVFP4_ERR_PAGE);
+        int64_t at = p * page_bytes + (int64_t)(gi & ((1 << a.ix.gshift) - 1)) * kGB;
+        if (!NVFP4_IN_BOUNDS(at + kGB - 1, good ? a.ix.num_pages * page_bytes : at + kGB, a.status)) at = 0;
+        from = of_head + at;
       }
-      return p;
+      there_next = __ballot_sync(0xFFFFFFFFu, good);
     };
-    int32_t next_ids = -1;
-    auto issue = [&](int i) {  // called by the whole warp
-      if ((i & 31) == 0) next_ids = fetch_ids(i);
-      const int32_t p = __shfl_sync(0xFFFFFFFFu, next_ids, i & 31);
-      if (lane == 0 && p >= 0) {
-        const int gi = gfirst + kAttnWarps * i;
-        const int st = i % kStages;
-        int64_t at = (((int64_t)p * a.ix.hkv + head) * gpp + gi % gpp) * kGB;
-        if (!NVFP4_IN_BOUNDS(at + kGB - 1, a.ix.num_pages * a.ix.hkv * gpp * kGB, a.status)) at = 0;
-        const uint8_t* from = a.pages + at;
-        mbar_arrive_expect_tx(&sh.bar[warp][st], kGB);
-        bulk_load(sh.ring[warp][st], from, kGB, &sh.bar[warp][st]);
-      }
+    auto issue = [&](int i, int st) {  // called by the whole warp, i in order
+      if ((i & 15) == 0) look_up(i);
+      const uint32_t two = (there_next >> (2 * (i & 15))) & 3u;
+      if (two == 0) return;
+      if (lane == 0) mbar_arrive_expect_tx(&sh.bar[warp][st], (uint32_t)__popc(two) * kGB);
+      __syncwarp();
+      if ((lane >> 1) == (i & 15) && ((there_next >> lane) & 1u))
+        bulk_load(sh.ring[warp][st] + (lane & 1) * kGB, from, kGB, &sh.bar[warp][st]);
     };
-    const int ahead = cnt < kStages - 1 ? cnt : kStages - 1;
-    for (int i = 0; i < ahead; ++i) issue(i);
-    int st = 0;
+    int ahead = 0, st_ahead = 0, st = 0;
+    for (; ahead < cnt && ahead < kStages - 1; ++ahead) {
+      issue(ahead, st_ahead++);
+      if ((ahead & 15) == 0) there = there_next;
+    }
     for (int i = 0; i < cnt; ++i) {
-      if (i + kStages - 1 < cnt) issue(i + kStages - 1);  // into the stage that the last iteration has read
-      if ((i & 31) == 0) ids = fetch_ids(i);
-      const int32_t page = __shfl_sync(0xFFFFFFFFu, ids, i & 31);
-      if (page < 0) {  // not a page: its tokens count as masked
-        if (++st == kStages) st = 0;
-        continue;
+      if ((i & 15) == 0) there = there_next;  // the look-up of this block ran at most kStages - 1 pairs ago
+      const uint32_t two = (there >> (2 * (i & 15))) & 3u;
+      if (ahead < cnt) {  // into the stage that the last trip has read
+        issue(ahead++, st_ahead);
+        if (++st_ahead == kStages) st_ahead = 0;
       }
-      if (!sh.abort && !mbar_wait_warp(&sh.bar[warp][st], (phase >> st) & 1u, &sh.abort, kAttnWaitNs))
-        if (lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
-      phase ^= 1u << st;
+      if (two) {
+        if (!wait(&sh.bar[warp][st], (phase >> st) & 1u) && lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
+        phase ^= 1u << st;
+      }
       const uint8_t* gr = sh.ring[warp][st];
       if (++st == kStages) st = 0;
+      if (two == 0) continue;
 
-      // S^T of 16 tokens
-      float s[NT][4];
+      // S^T of 32 tokens
+      float s[NT][2][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-      {
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) s[nt][y][0] = s[nt][y][1] = s[nt][y][2] = s[nt][y][3] = 0.0f;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
         uint32_t wa[kWords], wb[kWords];  // rows g and g + 8
-        const uint8_t* ka = gr + token_of(g) * (D / 2) + t * (D / 8);
-        const uint8_t* kb = gr + token_of(g + 8) * (D / 2) + t * (D / 8);
+        const uint8_t* k0 = gr + y * kGB;
+        const uint8_t* ka = k0 + token_of(g) * (D / 2) + t * (D / 8);
+        const uint8_t* kb = k0 + token_of(g + 8) * (D / 2) + t * (D / 8);
         uint32_t sa, sb;  // scale bytes of the lane's D/4 dimensions (two blocks, or one)
         if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(ka), y = *reinterpret_cast<const uint4*>(kb);
-          wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w;
-          wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[3] = y.w;
-          sa = *reinterpret_cast<const uint16_t*>(gr + 8 * D + token_of(g) * 8 + 2 * t);
-          sb = *reinterpret_cast<const uint16_t*>(gr + 8 * D + token_of(g + 8) * 8 + 2 * t);
+          const uint4 u = *reinterpret_cast<const uint4*>(ka), v = *reinterpret_cast<const uint4*>(kb);
+          wa[0] = u.x; wa[1] = u.y; wa[2] = u.z; wa[3] = u.w;
+          wb[0] = v.x; wb[1] = v.y; wb[2] = v.z; wb[3] = v.w;
+          sa = *reinterpret_cast<const uint16_t*>(k0 + 8 * D + token_of(g) * 8 + 2 * t);
+          sb = *reinterpret_cast<const uint16_t*>(k0 + 8 * D + token_of(g + 8) * 8 + 2 * t);
         } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(ka), y = *reinterpret_cast<const uint2*>(kb);
-          wa[0] = x.x; wa[1] = x.y;
-          wb[0] = y.x; wb[1] = y.y;
-          sa = gr[8 * D + token_of(g) * 4 + t];
-          sb = gr[8 * D + token_of(g + 8) * 4 + t];
+          const uint2 u = *reinterpret_cast<const uint2*>(ka), v = *reinterpret_cast<const uint2*>(kb);
+          wa[0] = u.x; wa[1] = u.y;
+          wb[0] = v.x; wb[1] = v.y;
+          sa = k0[8 * D + token_of(g) * 4 + t];
+          sb = k0[8 * D + token_of(g + 8) * 4 + t];
         }
 #pragma unroll
         for (int blk = 0; blk < D / 64; ++blk) {
@@ -251,10 +260,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
           const uint32_t fb = scales_to_half(__byte_perm(sb, 0, blk ? 0x4141 : 0x4040));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int w = 2 * blk + h;
+            const int x = 2 * blk + h;
             uint32_t pa[4], pb[4];
-            codes_to_half(wa[w], pa);
-            codes_to_half(wb[w], pb);
+            codes_to_half(wa[x], pa);
+            codes_to_half(wb[x], pb);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               pa[e] = hmul2(pa[e], fa);
@@ -262,36 +271,45 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_16816(s[nt], pa[0], pb[0], pa[1], pb[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
-              mma_16816(s[nt], pa[2], pb[2], pa[3], pb[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+              mma_16816(s[nt][y], pa[0], pb[0], pa[1], pb[1], qf[nt][4 * x], qf[nt][4 * x + 1]);
+              mma_16816(s[nt][y], pa[2], pb[2], pa[3], pb[3], qf[nt][4 * x + 2], qf[nt][4 * x + 3]);
             }
           }
         }
       }
 
       // scores in log2 units, mask, running maximum
-      const int tok0 = (gfirst + kAttnWarps * i) * kGranule;
-      const bool whole = tok0 >= all_lo && tok0 + kGranule <= all_hi;
+      const int tok0 = (gfirst + 2 * kAttnWarps * i) * kGranule;
+      const bool whole = tok0 >= all_lo && tok0 + 2 * kGranule <= all_hi && two == 3u;
       bool grow = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = e & 1;
-          s[nt][e] *= factor[nt][c];
-          if (!whole) {
-            const int tk = tok0 + token_of(g + (e & 2) * 4);
-            if (tk < lo[nt][c] || tk >= hi[nt][c]) s[nt][e] = -INFINITY;
-          }
-          grow |= s[nt][e] > m[nt][c] + kRescaleAt;
-        }
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][y][e] *= factor[nt][e & 1];
+      if (!whole) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tk = tok0 + kGranule * y + token_of(g + (e & 2) * 4), c = e & 1;
+              if (tk < lo[nt][c] || tk >= hi[nt][c] || !((two >> y) & 1u)) s[nt][y][e] = -INFINITY;
+            }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          grow |= fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2])) > m[nt][c] + kRescaleAt;
       if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(s[nt][c], s[nt][c + 2]);
+            float mx = fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2]));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
@@ -300,66 +318,67 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
             m[nt][c] = m1;
             l[nt][c] *= f;
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
-              o[nt][j][c] *= f;
-              o[nt][j][c + 2] *= f;
+            for (int x = 0; x < kSteps; ++x) {
+              o[nt][x][c] *= f;
+              o[nt][x][c + 2] *= f;
             }
           }
       }
       // P^T as B fragments: FP16 rounds p to 2^-11 of itself
-      uint32_t pf[NT][2];
+      uint32_t pf[NT][2][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
+        const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float mm = m[nt][e & 1];
-          p[e] = ex2(s[nt][e] - (mm == -INFINITY ? 0.0f : mm));
+        for (int y = 0; y < 2; ++y) {
+          const float p0 = ex2(s[nt][y][0] - m0), p1 = ex2(s[nt][y][1] - m1);
+          const float p2 = ex2(s[nt][y][2] - m0), p3 = ex2(s[nt][y][3] - m1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          pf[nt][y][0] = transpose_8x8(half2_bits(p0, p1));
+          pf[nt][y][1] = transpose_8x8(half2_bits(p2, p3));
         }
-        l[nt][0] += p[0] + p[2];
-        l[nt][1] += p[1] + p[3];
-        pf[nt][0] = transpose_8x8(half2_bits(p[0], p[1]));
-        pf[nt][1] = transpose_8x8(half2_bits(p[2], p[3]));
       }
 
-      // O^T += V^T P^T: m-tile j of a word holds dimensions 2j and 2j+1 of each lane's run
-      {
-        const uint8_t* v0 = gr + 9 * D;
-        const uint8_t* vs = gr + 17 * D;
+      // O^T += V^T P^T
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint8_t* v0 = gr + y * kGB + 9 * D;
+        const uint8_t* vs = gr + y * kGB + 17 * D;
         constexpr int kVWords = D / 64;
-        uint32_t w[4][kVWords], f[2];
+        uint32_t v[4][kVWords], f[2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int tk = token_of(2 * t + (k & 1) + (k & 2) * 4);
           if constexpr (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(v0 + tk * 64 + 8 * g);
-            w[k][0] = x.x;
-            w[k][1] = x.y;
+            const uint2 u = *reinterpret_cast<const uint2*>(v0 + tk * 64 + 8 * g);
+            v[k][0] = u.x;
+            v[k][1] = u.y;
           } else {
-            w[k][0] = *reinterpret_cast<const uint32_t*>(v0 + tk * 32 + 4 * g);
+            v[k][0] = *reinterpret_cast<const uint32_t*>(v0 + tk * 32 + 4 * g);
           }
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int ta = token_of(2 * t + 8 * k), tb = token_of(2 * t + 1 + 8 * k);
-          const uint32_t x = D == 128 ? vs[ta * 8 + g] : vs[ta * 4 + (g >> 1)];
-          const uint32_t y = D == 128 ? vs[tb * 8 + g] : vs[tb * 4 + (g >> 1)];
-          f[k] = scales_to_half(x | (y << 16));
+          const uint32_t u = D == 128 ? vs[ta * 8 + g] : vs[ta * 4 + (g >> 1)];
+          const uint32_t z = D == 128 ? vs[tb * 8 + g] : vs[tb * 4 + (g >> 1)];
+          f[k] = scales_to_half(u | (z << 16));
         }
 #pragma unroll
         for (int x = 0; x < kVWords; ++x) {  // eight dimensions of the lane's run at a time
           // the tokens' nibbles side by side: even dimensions, then odd ones, of two tokens in each byte
           uint32_t pa[2][4], pb[2][4];
-          codes_to_half((w[0][x] & 0x0F0F0F0Fu) | ((w[1][x] << 4) & 0xF0F0F0F0u), pa[0]);
-          codes_to_half(((w[0][x] >> 4) & 0x0F0F0F0Fu) | (w[1][x] & 0xF0F0F0F0u), pa[1]);
-          codes_to_half((w[2][x] & 0x0F0F0F0Fu) | ((w[3][x] << 4) & 0xF0F0F0F0u), pb[0]);
-          codes_to_half(((w[2][x] >> 4) & 0x0F0F0F0Fu) | (w[3][x] & 0xF0F0F0F0u), pb[1]);
+          codes_to_half((v[0][x] & 0x0F0F0F0Fu) | ((v[1][x] << 4) & 0xF0F0F0F0u), pa[0]);
+          codes_to_half(((v[0][x] >> 4) & 0x0F0F0F0Fu) | (v[1][x] & 0xF0F0F0F0u), pa[1]);
+          codes_to_half((v[2][x] & 0x0F0F0F0Fu) | ((v[3][x] << 4) & 0xF0F0F0F0u), pb[0]);
+          codes_to_half(((v[2][x] >> 4) & 0x0F0F0F0Fu) | (v[3][x] & 0xF0F0F0F0u), pb[1]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {  // m-tile: dimensions 8x + 2e (rows 0..7) and 8x + 2e + 1 (rows 8..15)
             const uint32_t a0 = hmul2(pa[0][e], f[0]), a1 = hmul2(pa[1][e], f[0]);
             const uint32_t a2 = hmul2(pb[0][e], f[1]), a3 = hmul2(pb[1][e], f[1]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][4 * x + e], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][4 * x + e], a0, a1, a2, a3, pf[nt][y][0], pf[nt][y][1]);
           }
         }
       }
@@ -456,25 +475,35 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       }
       __syncthreads();
       if (sh.last) {
-        auto part_of = [&](int64_t c) { return a.partial + (2 * c + (c == c0 ? 1 : 0)) * kPart; };
-        if (tid < kRows) {
+        // the parts' factors 2^(m_c - m) / l, a warp for each row, then O with eight parts' loads in flight
+        const int np = (int)(c1 - c0) + 1;
+        float* factor_of = &sh.join[0][0][0];  // [np][kRows]
+        auto part_of = [&](int c) { return a.partial + (2 * (c0 + c) + (c == 0 ? 1 : 0)) * kPart; };
+        for (int row = warp; row < kRows; row += kAttnWarps) {
           float mt = -INFINITY, lt = 0.0f;
-          for (int64_t c = c0; c <= c1; ++c) mt = fmaxf(mt, __ldcg(part_of(c) + kRows * D + tid));
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float mc = __ldcg(part_of(c) + kRows * D + tid);
-            lt += mc == -INFINITY ? 0.0f : __ldcg(part_of(c) + kRows * D + kRows + tid) * ex2(mc - mt);
+          for (int c = lane; c < np; c += 32) mt = fmaxf(mt, __ldcg(part_of(c) + kRows * D + row));
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, x));
+          for (int c = lane; c < np; c += 32) {
+            const float mc = __ldcg(part_of(c) + kRows * D + row);
+            const float f = mc == -INFINITY ? 0.0f : ex2(mc - mt);
+            factor_of[c * kRows + row] = f;
+            lt += f == 0.0f ? 0.0f : __ldcg(part_of(c) + kRows * D + kRows + row) * f;
           }
-          sh.m[tid] = mt;
-          sh.l[tid] = lt;
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, x);
+          if (lane == 0) {
+            sh.m[row] = mt;
+            sh.l[row] = lt;
+          }
         }
         __syncthreads();
         write_rows([&](int row, int d) {
           float2 x = make_float2(0.0f, 0.0f);
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float* p = part_of(c);
-            const float mc = __ldcg(p + kRows * D + row);
-            const float f = mc == -INFINITY ? 0.0f : ex2(mc - sh.m[row]);
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(p + row * D + d));
+#pragma unroll 8
+          for (int c = 0; c < np; ++c) {
+            const float f = factor_of[c * kRows + row];
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(part_of(c) + row * D + d));
             x.x += y.x * f;
             x.y += y.y * f;
           }

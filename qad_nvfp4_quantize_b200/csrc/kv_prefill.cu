@@ -227,7 +227,6 @@ NVFP4_DEVINL uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-NVFP4_DEVINL int uniform(int v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
 // Byte of 16-byte chunk c (0..7) of row r of half h (64 dimensions) in a 128-byte-swizzled tile.
 NVFP4_DEVINL uint32_t tile_chunk(int h, int r, int c) {
   return (uint32_t)(h * kTileTokens * 128 + r * 128 + ((c ^ (r & 7)) << 4));
@@ -289,19 +288,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   auto timed_out = [&]() {
     if (lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
   };
-  auto wait = [&](uint64_t* bar, uint32_t parity) {  // by the whole warp; a completed phase costs one poll
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    uint32_t spins = 0;
-    const int64_t t0 = clock64();
-    while (true) {
-      const bool done = mbar_try_wait(bar, parity);
-      if (__all_sync(0xFFFFFFFFu, done)) return true;
-      if ((++spins & 15u) == 0 && __any_sync(0xFFFFFFFFu, sh.abort || clock64() - t0 > kAttnWaitCycles)) {
-        sh.abort = 1;
-        return false;
-      }
-    }
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity, &sh.abort); };
   // place of K (2t) or V (2t + 1) in the ring of tiles, and the parity of its turn there
   auto place = [](uint32_t x) { return x % Sh::kTiles; };
   auto turn_of = [](uint32_t x) { return (x / Sh::kTiles) & 1; };
