@@ -399,9 +399,15 @@ class KVCache(NamedTuple):
     head_dim: int
 
 
+_page_bytes: dict = {}
+
+
 def kv_page_bytes(page_size: int, head_dim: int) -> int:
     """Bytes of one head's part of a page; 0 for sizes without a kernel."""
-    return int(lib().nvfp4_kv_page_bytes(page_size, head_dim))
+    got = _page_bytes.get((page_size, head_dim))
+    if got is None:
+        got = _page_bytes[page_size, head_dim] = int(lib().nvfp4_kv_page_bytes(page_size, head_dim))
+    return got
 
 
 def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int, k_g: torch.Tensor,
@@ -415,42 +421,62 @@ def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int, k_g: 
     return KVCache(pages, k_g, v_g, page_size, head_dim)
 
 
-def _ints(t: torch.Tensor, name: str, dev: torch.device, *shape) -> int:
-    """Checks a contiguous int32 tensor on dev (None in shape: any size); returns its address."""
-    if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous torch.int32 tensor on {dev}")
-    if t.dim() != len(shape) or any(want is not None and want != got for want, got in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+# The calls below are short on the GPU (some microseconds), so their checks and
+# look-ups are kept cheap on the host: device indices instead of device objects,
+# raw stream handles, no context manager unless another device is current.
+_INT32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+
+
+def _ints(t: torch.Tensor, name: str, index: int, *shape) -> int:
+    """Checks a contiguous int32 tensor on GPU `index` (None in shape: any size); returns its address."""
+    got = t.shape
+    if t.dtype is not _INT32 or t.get_device() != index or not t.is_contiguous() or len(got) != len(shape):
+        raise ValueError(f"{name} must be a contiguous torch.int32 tensor of {len(shape)} dimension(s) on cuda:{index}")
+    for want, have in zip(shape, got):
+        if want is not None and want != have:
+            raise ValueError(f"{name} must have shape {list(shape)}, got {list(got)}")
     return t.data_ptr()
 
 
-def _rows(x: torch.Tensor, name: str, dev: torch.device, heads: Optional[int], dim: int) -> int:
+def _rows(x: torch.Tensor, name: str, index: int, heads: Optional[int], dim: int) -> int:
     """Checks BF16 [tokens, heads, dim] whose tokens are contiguous (a part of a
     projection's output is); returns the elements from one token to the next."""
-    if x.dtype != torch.bfloat16 or x.device != dev or x.dim() != 3:
-        raise ValueError(f"{name} must be a torch.bfloat16 [tokens, heads, head_dim] tensor on {dev}")
+    if x.dtype is not _BF16 or x.get_device() != index or x.dim() != 3:
+        raise ValueError(f"{name} must be a torch.bfloat16 [tokens, heads, head_dim] tensor on cuda:{index}")
     n, h, d = x.shape
     if d != dim or (heads is not None and h != heads) or h == 0:
         raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim}], got {list(x.shape)}")
-    stride = x.stride()
-    if stride[2] != 1 or (h > 1 and stride[1] != d):
+    step, head, one = x.stride()
+    if one != 1 or (h > 1 and head != d):
         raise ValueError(f"{name}: the values of a token must be contiguous")
-    return stride[0] if n > 1 else h * d
+    return step if n > 1 else h * d
 
 
 def _kv_cache_of(cache: KVCache):
-    """Checks a cache; returns (device, pages, kv heads)."""
+    """Checks a cache; returns (device index, pages, kv heads, bytes of a page and head)."""
     pages = cache.pages
-    if pages.dim() != 3 or pages.dtype != torch.uint8 or not pages.is_cuda or not pages.is_contiguous():
+    index = pages.get_device()
+    if pages.dim() != 3 or pages.dtype is not torch.uint8 or index < 0 or not pages.is_contiguous():
         raise ValueError("cache.pages must be a contiguous uint8 CUDA tensor [num_pages, kv_heads, page bytes]")
-    dev = pages.device
-    nbytes = kv_page_bytes(cache.page_size, cache.head_dim)
-    if nbytes == 0 or pages.shape[2] != nbytes:
+    n, heads, nbytes = pages.shape
+    if nbytes == 0 or nbytes != kv_page_bytes(cache.page_size, cache.head_dim):
         raise ValueError(f"cache.pages does not fit page_size {cache.page_size} and head_dim {cache.head_dim}")
     for g in (cache.k_g, cache.v_g):
-        if g.dtype != torch.float32 or g.numel() != 1 or g.device != dev:
+        if g.dtype is not _F32 or g.numel() != 1 or g.get_device() != index:
             raise ValueError("cache.k_g and cache.v_g must be 1-element FP32 tensors on the cache's device")
-    return dev, pages.shape[0], pages.shape[1]
+    return index, n, heads, nbytes
+
+
+def _call(name: str, index: int, *args) -> None:
+    """A C entry point on GPU `index`, on torch's current stream there."""
+    fn = getattr(_lib or lib(), name)
+    if index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _check(st, name)
 
 
 # The attention's workspace begins with counters that are zero between calls.
@@ -461,19 +487,20 @@ _ATTN_COUNTERS = 2048
 _attn_ws: dict = {}
 
 
-def _attention_workspace(dev: torch.device) -> torch.Tensor:
-    if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(int(lib().nvfp4_paged_attention_workspace_bytes()), dtype=torch.uint8, device=dev)
-        ws[:_ATTN_COUNTERS].zero_()
-        return ws
-    stream = torch.cuda.current_stream(dev)
-    key = (dev.index, stream.cuda_stream)
-    entry = _attn_ws.get(key)
+def _attention_workspace(index: int) -> torch.Tensor:
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _attention_workspace(index)
+    key = (index, torch._C._cuda_getCurrentRawStream(index))
+    capturing = torch.cuda.is_current_stream_capturing()
+    entry = None if capturing else _attn_ws.get(key)
     if entry is None:
-        ws = torch.empty(int(lib().nvfp4_paged_attention_workspace_bytes()), dtype=torch.uint8, device=dev)
+        ws = torch.empty(int(lib().nvfp4_paged_attention_workspace_bytes()), dtype=torch.uint8, device=f"cuda:{index}")
         ws[:_ATTN_COUNTERS].zero_()
+        if capturing:
+            return ws
         with _ws_lock:
-            entry = _attn_ws.setdefault(key, (stream, ws))
+            entry = _attn_ws.setdefault(key, (torch.cuda.current_stream(index), ws))
     return entry[1]
 
 
@@ -483,18 +510,15 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
     the cache's pages (nvfp4_kv_append). ``cu_q`` [batch+1]: first row of each
     sequence; ``kv_len`` [batch]: cached tokens, the new ones included;
     ``block_table`` [batch, width]: pages of each sequence (all int32)."""
-    dev, num_pages, heads = _kv_cache_of(cache)
-    stride = _rows(k, "k", dev, heads, cache.head_dim)
-    if _rows(v, "v", dev, heads, cache.head_dim) != stride or v.shape != k.shape:
+    index, num_pages, heads, _ = _kv_cache_of(cache)
+    stride = _rows(k, "k", index, heads, cache.head_dim)
+    if _rows(v, "v", index, heads, cache.head_dim) != stride or v.shape != k.shape:
         raise ValueError("k and v must have the same shape and strides")
     batch = kv_len.shape[0]
-    args = (_ints(cu_q, "cu_q", dev, batch + 1), _ints(kv_len, "kv_len", dev, batch), batch,
-            _ints(block_table, "block_table", dev, batch, None), block_table.shape[1])
-    with torch.cuda.device(dev):
-        st = lib().nvfp4_kv_append(k.data_ptr(), v.data_ptr(), stride, k.shape[0], heads, cache.head_dim, *args,
-                                   cache.pages.data_ptr(), num_pages, cache.page_size, cache.k_g.data_ptr(),
-                                   cache.v_g.data_ptr(), _MODES[mode], _stream(dev))
-    _check(st, "nvfp4_kv_append")
+    _call("nvfp4_kv_append", index, k.data_ptr(), v.data_ptr(), stride, k.shape[0], heads, cache.head_dim,
+          _ints(cu_q, "cu_q", index, batch + 1), _ints(kv_len, "kv_len", index, batch), batch,
+          _ints(block_table, "block_table", index, batch, None), block_table.shape[1], cache.pages.data_ptr(), num_pages,
+          cache.page_size, cache.k_g.data_ptr(), cache.v_g.data_ptr(), _MODES[mode])
 
 
 def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
@@ -507,55 +531,51 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     positions; ``max_q``: the most new tokens of a sequence, if known (it
     chooses the kernel only). Returns (out BF16, lse FP32 [tokens, q_heads] or
     None)."""
-    dev, num_pages, heads = _kv_cache_of(cache)
+    index, num_pages, heads, _ = _kv_cache_of(cache)
     dim = cache.head_dim
-    stride = _rows(q, "q", dev, None, dim)
-    total, hq = q.shape[:2]
+    stride = _rows(q, "q", index, None, dim)
+    total, hq, _ = q.shape
     batch = kv_len.shape[0]
-    args = (_ints(cu_q, "cu_q", dev, batch + 1), _ints(kv_len, "kv_len", dev, batch), batch,
-            _ints(block_table, "block_table", dev, batch, None), block_table.shape[1])
+    seqs = (_ints(cu_q, "cu_q", index, batch + 1), _ints(kv_len, "kv_len", index, batch), batch,
+            _ints(block_table, "block_table", index, batch, None), block_table.shape[1])
     if out is None:
-        out = torch.empty((total, hq, dim), dtype=torch.bfloat16, device=dev)
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous torch.bfloat16 {list(q.shape)} tensor on {dev}")
-    if want_lse and lse_out is None:
-        lse_out = torch.empty((total, hq), dtype=torch.float32, device=dev)
-    elif lse_out is not None and (lse_out.shape != (total, hq) or lse_out.dtype != torch.float32 or
-                                  lse_out.device != dev or not lse_out.is_contiguous()):
-        raise ValueError(f"lse_out must be a contiguous torch.float32 [{total}, {hq}] tensor on {dev}")
+        out = torch.empty((total, hq, dim), dtype=_BF16, device=q.device)
+    elif out.shape != q.shape or out.dtype is not _BF16 or out.get_device() != index or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous torch.bfloat16 {list(q.shape)} tensor on cuda:{index}")
+    if lse_out is not None:
+        if lse_out.shape != (total, hq) or lse_out.dtype is not _F32 or lse_out.get_device() != index or \
+                not lse_out.is_contiguous():
+            raise ValueError(f"lse_out must be a contiguous torch.float32 [{total}, {hq}] tensor on cuda:{index}")
+    elif want_lse:
+        lse_out = torch.empty((total, hq), dtype=_F32, device=q.device)
     if max_q is None:
         max_q = 1 if total <= batch else 0
-    with torch.cuda.device(dev):
-        ws = _attention_workspace(dev)
-        st = lib().nvfp4_paged_attention(q.data_ptr(), stride, total, hq, heads, dim, *args, cache.pages.data_ptr(),
-                                         num_pages, cache.page_size, cache.k_g.data_ptr(), cache.v_g.data_ptr(),
-                                         dim ** -0.5 if scale is None else scale, int(causal), window, max_q,
-                                         out.data_ptr(), None if lse_out is None else lse_out.data_ptr(),
-                                         ws.data_ptr(), ws.numel(), _stream(dev))
-    _check(st, "nvfp4_paged_attention")
+    ws = _attention_workspace(index)
+    _call("nvfp4_paged_attention", index, q.data_ptr(), stride, total, hq, heads, dim, *seqs, cache.pages.data_ptr(),
+          num_pages, cache.page_size, cache.k_g.data_ptr(), cache.v_g.data_ptr(), dim ** -0.5 if scale is None else scale,
+          int(causal), window, max_q, out.data_ptr(), None if lse_out is None else lse_out.data_ptr(), ws.data_ptr(),
+          ws.numel())
     return out, lse_out
 
 
 def kv_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor) -> None:
     """Copy page src[i] to page dst[i] (int32; negative: skipped). The dst pages
     are distinct and none of them is a src (nvfp4_kv_copy_pages)."""
-    dev, num_pages, heads = _kv_cache_of(cache)
+    index, num_pages, heads, nbytes = _kv_cache_of(cache)
     n = src.shape[0]
-    args = _ints(src, "src", dev, n), _ints(dst, "dst", dev, n), n
-    with torch.cuda.device(dev):
-        st = lib().nvfp4_kv_copy_pages(cache.pages.data_ptr(), num_pages, heads * cache.pages.shape[2], *args,
-                                       _stream(dev))
-    _check(st, "nvfp4_kv_copy_pages")
+    _call("nvfp4_kv_copy_pages", index, cache.pages.data_ptr(), num_pages, heads * nbytes, _ints(src, "src", index, n),
+          _ints(dst, "dst", index, n), n)
 
 
 def _pool(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor, page_size: int):
-    """Checks a pool's state; returns (device, the C calls' leading arguments)."""
-    if not refs.is_cuda:
+    """Checks a pool's state; returns (device index, the C calls' leading arguments)."""
+    index = refs.get_device()
+    if index < 0:
         raise ValueError("refs must be a CUDA tensor")
-    dev = refs.device
     slots = seq_len.shape[0]
-    return dev, (_ints(refs, "refs", dev, None), refs.shape[0], _ints(block_table, "block_table", dev, slots, None),
-                 slots, block_table.shape[1], _ints(seq_len, "seq_len", dev, slots), page_size)
+    return index, (_ints(refs, "refs", index, None), refs.shape[0],
+                   _ints(block_table, "block_table", index, slots, None), slots, block_table.shape[1],
+                   _ints(seq_len, "seq_len", index, slots), page_size)
 
 
 def kv_fork(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor, parent: torch.Tensor,
@@ -563,25 +583,20 @@ def kv_fork(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor
     """Make slot child[i] a copy of slot parent[i] (nvfp4_kv_fork). Updates the
     pool's state and returns (src, dst): the part pages to copy with
     kv_copy_pages, in every layer's cache."""
-    dev, pool = _pool(refs, block_table, seq_len, page_size)
+    index, pool = _pool(refs, block_table, seq_len, page_size)
     n = parent.shape[0]
-    args = _ints(parent, "parent", dev, n), _ints(child, "child", dev, n), n
-    src, dst = torch.empty((2, n), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        st = lib().nvfp4_kv_fork(*pool, *args, src.data_ptr(), dst.data_ptr(), _stream(dev))
-    _check(st, "nvfp4_kv_fork")
+    src, dst = torch.empty_like(parent), torch.empty_like(parent)
+    _call("nvfp4_kv_fork", index, *pool, _ints(parent, "parent", index, n), _ints(child, "child", index, n), n,
+          _ints(src, "src", index, n), dst.data_ptr())
     return src, dst
 
 
 def kv_free(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor, slots: torch.Tensor,
             page_size: int) -> None:
     """Free the named slots (nvfp4_kv_free)."""
-    dev, pool = _pool(refs, block_table, seq_len, page_size)
+    index, pool = _pool(refs, block_table, seq_len, page_size)
     n = slots.shape[0]
-    which = _ints(slots, "slots", dev, n)
-    with torch.cuda.device(dev):
-        st = lib().nvfp4_kv_free(*pool, which, n, _stream(dev))
-    _check(st, "nvfp4_kv_free")
+    _call("nvfp4_kv_free", index, *pool, _ints(slots, "slots", index, n), n)
 
 
 def kv_compact(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor, page_size: int,
@@ -590,20 +605,20 @@ def kv_compact(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Ten
     (refs, block_table, src, dst, live): the state after the moves (new tensors
     unless refs_out / table_out are given, which may be the inputs), the moves
     for kv_copy_pages (-1 behind the last) and the number of used pages [1]."""
-    dev, pool = _pool(refs, block_table, seq_len, page_size)
+    index, pool = _pool(refs, block_table, seq_len, page_size)
     pages = refs.shape[0]
     refs_out = torch.empty_like(refs) if refs_out is None else refs_out
     table_out = torch.empty_like(block_table) if table_out is None else table_out
-    outs = _ints(refs_out, "refs_out", dev, pages), _ints(table_out, "table_out", dev, *block_table.shape)
     cap = max(1, pages // 2)
-    src, dst = torch.empty((2, cap), dtype=torch.int32, device=dev)
-    live = torch.empty(1, dtype=torch.int32, device=dev)
     nbytes = int(lib().nvfp4_kv_compact_workspace_bytes(pages))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        st = lib().nvfp4_kv_compact(*pool, *outs, src.data_ptr(), dst.data_ptr(), live.data_ptr(), ws.data_ptr(),
-                                    nbytes, _stream(dev))
-    _check(st, "nvfp4_kv_compact")
+    # the moves, the count and the workspace (16-byte aligned) from one allocation
+    at = 2 * cap + 4 + (-2 * cap) % 4
+    got = torch.empty(at + nbytes // 4 + 1, dtype=_INT32, device=refs.device)
+    src, dst, live = got[:cap], got[cap:2 * cap], got[2 * cap:2 * cap + 1]
+    base = got.data_ptr()
+    _call("nvfp4_kv_compact", index, *pool, _ints(refs_out, "refs_out", index, pages),
+          _ints(table_out, "table_out", index, *block_table.shape), base, base + 4 * cap, base + 8 * cap, base + 4 * at,
+          nbytes)
     return refs_out, table_out, src, dst, live
 
 
