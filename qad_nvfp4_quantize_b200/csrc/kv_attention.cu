@@ -34,6 +34,9 @@ namespace nvfp4 {
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;
+// A work is not cut into pieces of less than this many granules while CTAs are
+// left over: joining two pieces costs as long as a CTA needs for about so many.
+constexpr int kCoarseGranules = 96;
 
 template <int D, int NT>
 struct AttnShared {
@@ -43,8 +46,9 @@ struct AttnShared {
   union {
     uint8_t ring[kAttnWarps][kStages][2 * granule_bytes(D)];
     float join[kAttnWarps][kRows][kPad];
-    PartShared part;
+    PartScratch scratch;
   };
+  Part<8 * NT> part;
   uint64_t bar[kAttnWarps][kStages];
   float wm[kAttnWarps][kRows], wl[kAttnWarps][kRows];
   float m[kRows], l[kRows];
@@ -76,7 +80,7 @@ __host__ __device__ constexpr int token_of(int i) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_kernel(const AttnArgs a, int min_units) {
+__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_kernel(const AttnArgs a) {
   using Sh = AttnShared<D, NT>;
   extern __shared__ __align__(128) uint8_t attn_smem[];
   Sh& sh = *reinterpret_cast<Sh*>(attn_smem);
@@ -90,18 +94,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
   if (tid == 0) sh.abort = 0;
   fence_barrier_init();
 
-  // ---- this CTA's part of the list of units
-  int64_t per = 0;
-  auto first_unit = [&](int64_t total) {
-    per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < min_units) per = min_units;
-    return per * blockIdx.x;
-  };
-  find_part<kRows, 1, kAttnThreads>(a, sh.part, first_unit);
-  const int64_t total = sh.part.total, u0 = first_unit(total), u1 = u0 + per < total ? u0 + per : total;
+  find_part<kRows, 1, kCoarseGranules, kAttnThreads>(a, sh.scratch, sh.part);
+  const int64_t u0 = sh.part.u0, u1 = sh.part.u1, per = sh.part.per;
   if (u0 >= u1) return;
-  WorkCursor<kRows, 1> w;
-  w.start(a, sh.part.b, sh.part.tile, sh.part.base, u0);
+  WorkCursor<kRows> w = sh.part.cursor;
   fence_proxy_async_smem();
   __syncthreads();  // the search's scratch lies over the ring
   uint32_t phase = 0;  // parity bit of each stage of this warp's ring
@@ -109,27 +105,29 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
   const float kg = *a.k_g, vg = *a.v_g;
 
   for (int64_t u = u0;;) {
-    const int j0 = (int)(u - w.w0);
-    const int j1 = (int)(u1 - w.w0 < w.n ? u1 - w.w0 : w.n);
-    u = w.w0 + j1;
+    const int unit0 = (int)(u - w.w0), unit1 = (int)(u1 - w.w0 < w.n ? u1 - w.w0 : w.n);
+    const bool whole_work = unit0 == 0 && unit1 == w.n;
+    u = w.w0 + unit1;
     const KvSeq& seq = w.seq;
-    const int tile = w.tile, head = w.head, n = w.n, b = w.b;
+    const int tile = w.tile, head = w.head, b = w.b;
+    const int j0 = unit0 * w.unit, j1 = unit1 * w.unit < w.span.n ? unit1 * w.unit : w.span.n;  // granules
 
     // ---- queries: B fragments of Q^T, row r = tile*kRows + 8*nt + g of the head's rows
     uint32_t qf[NT][2 * kSteps];
     float factor[NT][2];        // score units of columns 2t, 2t+1
     int32_t lo[NT][2], hi[NT][2];
     int32_t all_lo = 0, all_hi = 0x7FFFFFFF;  // tokens that every row of the tile sees
-    const int64_t nrows = (int64_t)seq.rows * a.group;
+    const int32_t nrows = seq.rows * a.group;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int64_t r = (int64_t)tile * kRows + 8 * nt + g;
+      const int32_t r = tile * kRows + 8 * nt + g;
       uint32_t raw[D / 8];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) raw[i] = 0;
       if (r < nrows) {
-        const int64_t tok = seq.row0 + r / a.group, hq = (int64_t)head * a.group + r % a.group;
-        const uint4* q4 = reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + hq * D + t * (D / 4));
+        const int32_t tok = r / a.group, hq = head * a.group + r - tok * a.group;
+        const uint4* q4 =
+            reinterpret_cast<const uint4*>(a.q + (seq.row0 + tok) * a.q_stride + (int64_t)hq * D + t * (D / 4));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint4 v = ld_stream(q4 + i);
@@ -148,11 +146,11 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
                                scale_exp2(__uint_as_float(raw[e] & 0xFFFF0000u), ex));
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int64_t rc = (int64_t)tile * kRows + 8 * nt + 2 * t + c;
+        const int32_t rc = tile * kRows + 8 * nt + 2 * t + c;
         const int ec = __shfl_sync(0xFFFFFFFFu, ex, (2 * t + c) * 4);
         factor[nt][c] = scale_exp2(a.scale * kg * kLog2e, kValueExp - ec);
         Visible v{0, 0};
-        if (rc < nrows) v = visible((int64_t)seq.len - seq.rows + rc / a.group, seq.len, a.causal, a.window);
+        if (rc < nrows) v = visible(seq.len - seq.rows + rc / a.group, seq.len, a.causal, a.window);
         lo[nt][c] = v.lo;
         hi[nt][c] = v.hi;
         if (rc < nrows) {
@@ -425,14 +423,13 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     __syncthreads();
 
     // ---- a whole work is written out; a part goes to the workspace, and the last part joins them
-    const bool whole_work = j0 == 0 && j1 == n;
     auto write_rows = [&](auto&& value) {  // value(row, d) = unnormalised sum; sh.m, sh.l as joined
       for (int e = tid; e < kRows * (D / 2); e += kAttnThreads) {
         const int row = e / (D / 2), d = (e % (D / 2)) * 2;
-        const int64_t r = (int64_t)tile * kRows + row;
+        const int32_t r = tile * kRows + row;
         if (r >= nrows) continue;
-        const int64_t tok = seq.row0 + r / a.group, hq = (int64_t)head * a.group + r % a.group;
-        const int64_t at = tok * a.ix.hkv * a.group + hq;
+        const int32_t tok = r / a.group, hq = head * a.group + r - tok * a.group;
+        const int64_t at = (seq.row0 + tok) * a.ix.hkv * a.group + hq;
         const float lt = sh.l[row];
         const float f = lt == 0.0f ? 0.0f : kValueScale * vg / lt;  // no visible token: zeros
         const float2 x = value(row, d);
@@ -455,7 +452,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     if (whole_work) {
       write_rows(joined);
     } else {
-      float* part = a.partial + (2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0)) * kPart;
+      float* part = a.partial + (2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0)) * kPart;
       for (int e = tid; e < kRows * (D / 2); e += kAttnThreads) {
         const int row = e / (D / 2), d = (e % (D / 2)) * 2;
         *reinterpret_cast<float2*>(part + row * D + d) = joined(row, d);
@@ -466,7 +463,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       }
       __threadfence();
       __syncthreads();
-      const int64_t c0 = w.w0 / per, c1 = (w.w0 + n - 1) / per;  // the CTAs that share the work
+      const int64_t c0 = w.w0 / per, c1 = (w.w0 + w.n - 1) / per;  // the CTAs that share the work
       if (tid == 0) {
         const int last = atomicAdd(&a.counters[c0], 1) == (int)(c1 - c0);
         if (last) a.counters[c0] = 0;  // ready for the next call
@@ -535,7 +532,7 @@ cudaError_t launch_rows(AttnArgs a, int num_sms, cudaStream_t s) {
   const int64_t want = (NT == 1 ? 2 : 1) * (int64_t)num_sms;
   const int grid = (int)(want < kMaxAttnCtas ? want : kMaxAttnCtas);
   note_launch();
-  kv_attention_kernel<D, NT><<<grid, kAttnThreads, sizeof(Sh), s>>>(a, 2 * kAttnWarps);
+  kv_attention_kernel<D, NT><<<grid, kAttnThreads, sizeof(Sh), s>>>(a);
   return cudaGetLastError();
 }
 

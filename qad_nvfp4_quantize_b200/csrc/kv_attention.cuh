@@ -119,7 +119,7 @@ NVFP4_DEVINL bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abo
 // ---------------------------------------------------------------------------
 // Work list. A work is one KV head of one tile of kRows query rows of one
 // sequence (row r = new token r / group, query head r % group of the KV head);
-// its units are runs of kUnit granules that some row of the tile sees, at least
+// its units are runs of `unit` granules that some row of the tile sees, at least
 // one (a tile that sees nothing still writes its rows). The works of a launch
 // in order (sequence, tile, head) and their units form one list, from which
 // every CTA takes an equal part: the lengths are read on the device, so ragged
@@ -143,131 +143,18 @@ template <int kRows>
 NVFP4_DEVINL int tiles_of(const AttnArgs& a, const KvSeq& s) {
   return (s.rows * a.group + (kRows - 1)) / kRows;
 }
-template <int kUnit>
-NVFP4_DEVINL int units_of(const Span& s) {
-  return s.n > 0 ? (s.n + kUnit - 1) / kUnit : 1;
-}
+NVFP4_DEVINL int units_of(const Span& s, int unit) { return s.n > unit ? (s.n + unit - 1) / unit : 1; }
 
-constexpr int kStoredSums = 512, kLongList = 64, kLongTiles = 16;
+constexpr int kStoredSums = 256, kLongList = 64, kLongTiles = 16;
 
-// Scratch of find_part (may lie over buffers that are not in use yet).
-struct PartShared {
-  int64_t sums[kStoredSums];
-  int64_t warp_total[32];
-  int32_t long_seq[kLongList];
-  int32_t long_count;
-  int64_t total, base;
-  int32_t b, tile;
-};
-
-// The units in all, and the (sequence, tile) that unit `u0(total)` lies in with
-// the index of that tile's first unit. Called by all kThreads threads; a thread
-// counts a sequence, a warp one of many tiles.
-template <int kRows, int kUnit, int kThreads, class First>
-NVFP4_DEVINL void find_part(const AttnArgs& a, PartShared& sh, First first) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto count = [&](const KvSeq& s, int t0, int step) {
-    int64_t u = 0;
-    const int tiles = tiles_of<kRows>(a, s);
-    for (int t = t0; t < tiles; t += step) u += units_of<kUnit>(tile_span<kRows>(a, s, t));
-    return u * a.ix.hkv;
-  };
-  if (tid == 0) sh.long_count = 0;
-  __syncthreads();
-  int64_t mine = 0;
-  for (int b = tid; b < a.ix.batch; b += kThreads) {
-    const KvSeq s = kv_sequence(a.ix, b, a.status);
-    if (tiles_of<kRows>(a, s) > kLongTiles && b < kStoredSums) {
-      const int i = atomicAdd(&sh.long_count, 1);
-      if (i < kLongList) {
-        sh.long_seq[i] = b;
-        continue;
-      }
-    }
-    const int64_t u = count(s, 0, 1);
-    if (b < kStoredSums) sh.sums[b] = u;
-    mine += u;
-  }
-  __syncthreads();
-  const int longs = sh.long_count < kLongList ? sh.long_count : kLongList;
-  for (int i = warp; i < longs; i += kThreads / 32) {
-    const int b = sh.long_seq[i];
-    int64_t u = count(kv_sequence(a.ix, b, nullptr), lane, 32);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
-    if (lane == 0) {
-      sh.sums[b] = u;
-      mine += u;
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-  if (lane == 0) sh.warp_total[warp] = mine;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t total = lane < kThreads / 32 ? sh.warp_total[lane] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    const int64_t u0 = first(total);
-    // inclusive scan of 32 values; the lane whose part of the list holds u0
-    int64_t base = 0;
-    auto locate = [&](int64_t v) {
-      int64_t incl = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      const unsigned at = __ballot_sync(0xFFFFFFFFu, base + incl > u0);
-      const int src = at ? __ffs(at) - 1 : 31;
-      base += __shfl_sync(0xFFFFFFFFu, at ? incl - v : incl, src);
-      return at ? src : -1;
-    };
-    if (u0 < total) {
-      int b = -1, tile = -1;
-      for (int b0 = 0; b < 0 && b0 < a.ix.batch; b0 += 32) {
-        const int x = b0 + lane;
-        int64_t v = 0;
-        if (x < a.ix.batch) v = x < kStoredSums ? sh.sums[x] : count(kv_sequence(a.ix, x, nullptr), 0, 1);
-        const int src = locate(v);
-        if (src >= 0) b = b0 + src;
-      }
-      const KvSeq s = b < 0 ? KvSeq{0, 0, 0} : kv_sequence(a.ix, b, nullptr);
-      const int tiles = tiles_of<kRows>(a, s);
-      for (int t0 = 0; tile < 0 && t0 < tiles; t0 += 32) {
-        const int x = t0 + lane;
-        const int src = locate(x < tiles ? (int64_t)units_of<kUnit>(tile_span<kRows>(a, s, x)) * a.ix.hkv : 0);
-        if (src >= 0) tile = t0 + src;
-      }
-      if (tile < 0) total = 0;  // lengths that another stream changes meanwhile: no work rather than a wrong one
-      if (lane == 0) {
-        sh.b = b;
-        sh.tile = tile;
-        sh.base = base;
-      }
-    }
-    if (lane == 0) sh.total = total;
-  }
-  __syncthreads();
-}
-
-// A CTA's place in the list, moved from work to work. Every thread keeps its
-// own copy (the values are the same in all of them).
-template <int kRows, int kUnit>
+// A CTA's place in the list, moved from work to work.
+template <int kRows>
 struct WorkCursor {
   KvSeq seq;
   Span span;
   int b, tile, head, n;  // n: units of the work
   int64_t w0;            // the work's first unit
-  NVFP4_DEVINL void start(const AttnArgs& a, int b_, int tile_, int64_t tile_base, int64_t u) {
-    b = b_;
-    tile = tile_;
-    seq = kv_sequence(a.ix, b, nullptr);
-    span = tile_span<kRows>(a, seq, tile);
-    n = units_of<kUnit>(span);
-    head = (int)((u - tile_base) / n);
-    w0 = tile_base + (int64_t)head * n;
-  }
+  int unit;
   NVFP4_DEVINL bool next(const AttnArgs& a) {  // false behind the last work
     w0 += n;
     if (++head < a.ix.hkv) return true;
@@ -280,9 +167,156 @@ struct WorkCursor {
       } while (seq.rows == 0);
     }
     span = tile_span<kRows>(a, seq, tile);
-    n = units_of<kUnit>(span);
+    n = units_of(span, unit);
     return true;
   }
 };
+
+// Where a CTA begins: filled by find_part (its scratch may lie over buffers that
+// are not in use yet).
+template <int kRows>
+struct Part {
+  WorkCursor<kRows> cursor;
+  int64_t u0, u1, per;  // this CTA's units [u0, u1); units of a CTA
+};
+struct PartScratch {
+  int64_t sums[2][kStoredSums];
+  int64_t warp_total[2][32];
+  int32_t long_seq[kLongList];
+  int32_t long_count;
+};
+
+// This CTA's part of the list, called by all kThreads threads. Units are kFine
+// granules, or kCoarse where that leaves less than kCoarse granules to a CTA:
+// then works are not cut into smaller pieces than that (kCoarse a multiple of
+// kFine). A thread counts a sequence, a warp one of many tiles.
+template <int kRows, int kFine, int kCoarse, int kThreads>
+NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& part) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  struct Two {
+    int64_t fine, coarse;
+  };
+  auto count = [&](const KvSeq& s, int t0, int step) {
+    Two u{0, 0};
+    const int tiles = tiles_of<kRows>(a, s);
+    for (int t = t0; t < tiles; t += step) {
+      const Span span = tile_span<kRows>(a, s, t);
+      u.fine += units_of(span, kFine);
+      u.coarse += units_of(span, kCoarse);
+    }
+    return Two{u.fine * a.ix.hkv, u.coarse * a.ix.hkv};
+  };
+  auto warp_sum = [&](Two& u) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      u.fine += __shfl_xor_sync(0xFFFFFFFFu, u.fine, o);
+      if (kCoarse != kFine) u.coarse += __shfl_xor_sync(0xFFFFFFFFu, u.coarse, o);
+    }
+  };
+  if (tid == 0) sh.long_count = 0;
+  __syncthreads();
+  Two mine{0, 0};
+  for (int b = tid; b < a.ix.batch; b += kThreads) {
+    const KvSeq s = kv_sequence(a.ix, b, a.status);
+    if (tiles_of<kRows>(a, s) > kLongTiles && b < kStoredSums) {
+      const int i = atomicAdd(&sh.long_count, 1);
+      if (i < kLongList) {
+        sh.long_seq[i] = b;
+        continue;
+      }
+    }
+    const Two u = count(s, 0, 1);
+    if (b < kStoredSums) {
+      sh.sums[0][b] = u.fine;
+      sh.sums[1][b] = u.coarse;
+    }
+    mine.fine += u.fine;
+    mine.coarse += u.coarse;
+  }
+  __syncthreads();
+  const int longs = sh.long_count < kLongList ? sh.long_count : kLongList;
+  for (int i = warp; i < longs; i += kThreads / 32) {
+    const int b = sh.long_seq[i];
+    Two u = count(kv_sequence(a.ix, b, nullptr), lane, 32);
+    warp_sum(u);
+    if (lane == 0) {
+      sh.sums[0][b] = u.fine;
+      sh.sums[1][b] = u.coarse;
+      mine.fine += u.fine;
+      mine.coarse += u.coarse;
+    }
+  }
+  warp_sum(mine);
+  if (lane == 0) {
+    sh.warp_total[0][warp] = mine.fine;
+    sh.warp_total[1][warp] = mine.coarse;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    Two all{0, 0};
+    if (lane < kThreads / 32) all = Two{sh.warp_total[0][lane], sh.warp_total[1][lane]};
+    warp_sum(all);
+    const bool coarse = kCoarse != kFine && all.fine * kFine < (int64_t)gridDim.x * kCoarse;
+    const int unit = coarse ? kCoarse : kFine;
+    const int64_t total = coarse ? all.coarse : all.fine;
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x, u0 = per * blockIdx.x;
+    int64_t base = 0;
+    // the lane whose part of the list, 32 values on from `base`, holds u0
+    auto locate = [&](int64_t v) {
+      int64_t incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const unsigned at = __ballot_sync(0xFFFFFFFFu, base + incl > u0);
+      const int src = at ? __ffs(at) - 1 : 31;
+      base += __shfl_sync(0xFFFFFFFFu, at ? incl - v : incl, src);
+      return at ? src : -1;
+    };
+    int b = -1, tile = -1;
+    KvSeq s{0, 0, 0};
+    if (u0 < total) {
+      for (int b0 = 0; b < 0 && b0 < a.ix.batch; b0 += 32) {
+        const int x = b0 + lane;
+        int64_t v = 0;
+        if (x < kStoredSums && x < a.ix.batch) {
+          v = sh.sums[coarse][x];
+        } else if (x < a.ix.batch) {
+          const Two u = count(kv_sequence(a.ix, x, nullptr), 0, 1);
+          v = coarse ? u.coarse : u.fine;
+        }
+        const int src = locate(v);
+        if (src >= 0) b = b0 + src;
+      }
+      if (b >= 0) s = kv_sequence(a.ix, b, nullptr);
+      const int tiles = tiles_of<kRows>(a, s);
+      if (tiles == 1) tile = 0;
+      for (int t0 = 0; tile < 0 && t0 < tiles; t0 += 32) {
+        const int x = t0 + lane;
+        const int src = locate(x < tiles ? (int64_t)units_of(tile_span<kRows>(a, s, x), unit) * a.ix.hkv : 0);
+        if (src >= 0) tile = t0 + src;
+      }
+    }
+    if (lane == 0) {
+      WorkCursor<kRows>& c = part.cursor;
+      c.unit = unit;
+      part.per = per;
+      part.u0 = u0;
+      // (no tile: the lengths changed under way, from another stream; no work rather than a wrong one)
+      part.u1 = tile < 0 ? u0 : u0 + per < total ? u0 + per : total;
+      if (tile >= 0) {
+        c.b = b;
+        c.tile = tile;
+        c.seq = s;
+        c.span = tile_span<kRows>(a, s, tile);
+        c.n = units_of(c.span, unit);
+        c.head = (int)((u0 - base) / c.n);
+        c.w0 = base + (int64_t)c.head * c.n;
+      }
+    }
+  }
+  __syncthreads();
+}
 
 }  // namespace nvfp4

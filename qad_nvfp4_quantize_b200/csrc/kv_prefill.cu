@@ -51,15 +51,15 @@ struct PreShared {
   uint8_t kv[kTiles][kTile];                         // K and V tiles in turn: K0 V0 K1 V1 ...
   union {
     uint8_t q[2][kTile];
-    PartShared part;
+    PartScratch scratch;
   };
   uint8_t codes[kStages][kUnitGranules][granule_bytes(D)];
   uint64_t codes_full[kStages], codes_empty[kStages];
   uint32_t there[kStages];  // bit g: granule g of the tile is there (within the span, on a page of the pool)
   uint64_t full[kTiles], empty[kTiles];
   uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], group[2];
-  WorkCursor<kPreRows, kUnitGranules> cursor[kPreThreads / 32];  // one per warp: no register is spent on it
-  int64_t u1, per;
+  Part<kPreRows> part;
+  WorkCursor<kPreRows> cursor[kPreThreads / 32];  // one per warp: no register is spent on it
   uint32_t tmem;
   int last[2];
   volatile int abort;
@@ -262,20 +262,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     sh.abort = 0;
     fence_barrier_init();
   }
-  int64_t per = 0;
-  auto first_unit = [&](int64_t total) {
-    per = (total + gridDim.x - 1) / gridDim.x;
-    return per * blockIdx.x;
-  };
-  find_part<kPreRows, kUnitGranules, kPreThreads>(a, sh.part, first_unit);
-  const int64_t total = sh.part.total, u0 = first_unit(total);
-  if (u0 >= total) return;
-  WorkCursor<kPreRows, kUnitGranules>& w = sh.cursor[warp];
-  if (lane == 0) w.start(a, sh.part.b, sh.part.tile, sh.part.base, u0);
-  if (tid == 0) {
-    sh.u1 = u0 + per < total ? u0 + per : total;
-    sh.per = per;
-  }
+  find_part<kPreRows, kUnitGranules, kUnitGranules, kPreThreads>(a, sh.scratch, sh.part);
+  if (sh.part.u0 >= sh.part.u1) return;
+  const int64_t u0 = sh.part.u0;
+  WorkCursor<kPreRows>& w = sh.cursor[warp];
+  if (lane == 0) w = sh.part.cursor;
   fence_proxy_async_smem();
   if (warp == 12) {
     tmem_alloc(&sh.tmem, 512);
@@ -295,11 +286,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   // units of the work that are this CTA's: its part begins at u0 and at the first unit of every later work
   // (the reductions make the values warp-uniform to the compiler as well)
   auto from_unit = [&]() { return uniform((int)(w.w0 < u0 ? u0 - w.w0 : 0)); };
-  auto to_unit = [&]() { return uniform((int)(sh.u1 - w.w0 < w.n ? sh.u1 - w.w0 : (int64_t)w.n)); };
+  auto to_unit = [&]() { return uniform((int)(sh.part.u1 - w.w0 < w.n ? sh.part.u1 - w.w0 : (int64_t)w.n)); };
   auto next_work = [&]() {  // the warp's cursor moves on; false at the end of the part
     __syncwarp();
     int more = 0;
-    if (lane == 0) more = w.w0 + w.n < sh.u1 && w.next(a);
+    if (lane == 0) more = w.w0 + w.n < sh.part.u1 && w.next(a);
     __syncwarp();
     return __any_sync(0xFFFFFFFFu, more) != 0;
   };
@@ -497,7 +488,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           }
           __threadfence();
           if (!(ok = meet())) break;
-          const int64_t c0 = w.w0 / sh.per, c1 = (w.w0 + w.n - 1) / sh.per;
+          const int64_t c0 = w.w0 / sh.part.per, c1 = (w.w0 + w.n - 1) / sh.part.per;
           if (row == 0) {
             const int last = atomicAdd(&a.counters[2 * c0 + i], 1) == (int)(c1 - c0);
             if (last) a.counters[2 * c0 + i] = 0;
