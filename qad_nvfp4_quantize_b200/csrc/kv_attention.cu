@@ -37,6 +37,7 @@ constexpr int kAttnThreads = kAttnWarps * 32;
 // A work is not cut into pieces of less than this many granules while CTAs are
 // left over: joining two pieces costs as long as a CTA needs for about so many.
 constexpr int kCoarseGranules = 96;
+constexpr int kMaxAttnCtas = 320;
 
 template <int D, int NT>
 struct AttnShared {
@@ -46,6 +47,7 @@ struct AttnShared {
   union {
     uint8_t ring[kAttnWarps][kStages][2 * granule_bytes(D)];
     float join[kAttnWarps][kRows][kPad];
+    float parts[2][kMaxAttnCtas][kRows];
     PartScratch scratch;
   };
   Part<8 * NT> part;
@@ -112,6 +114,45 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     const int tile = w.tile, head = w.head, b = w.b;
     const int j0 = unit0 * w.unit, j1 = unit1 * w.unit < w.span.n ? unit1 * w.unit : w.span.n;  // granules
 
+    // ---- this warp's pairs of granules j0 + 2*(warp + 8*i) and the next one; the first ones are fetched while the
+    // queries are prepared
+    const int cnt = uniform(w.span.n > 0 && j1 - j0 > 2 * warp ? (j1 - j0 - 2 * warp + 2 * kAttnWarps - 1) / (2 * kAttnWarps) : 0);
+    const int gfirst = w.span.g0 + j0 + 2 * warp, gend = w.span.g0 + j1;
+    const int32_t* table = a.ix.table + (int64_t)b * a.ix.width;
+    const int64_t page_bytes = ((int64_t)a.ix.hkv << a.ix.gshift) * kGB;
+    const uint8_t* of_head = a.pages + ((int64_t)head << a.ix.gshift) * kGB;
+    // Lane x of a block of 16 pairs looks after granule x & 1 of pair x >> 1: where it lies, and whether it is there
+    // (within the span, on a page of the pool; else its tokens count as masked).
+    const uint8_t* from = nullptr;
+    uint32_t there = 0, there_next = 0;
+    auto look_up = [&](int i0) {
+      const int i = i0 + (lane >> 1), gi = gfirst + 2 * kAttnWarps * i + (lane & 1);
+      bool good = i < cnt && gi < gend && NVFP4_IN_BOUNDS(gi >> a.ix.gshift, a.ix.width, a.status);
+      if (good) {
+        const int32_t p = table[gi >> a.ix.gshift];
+        good = p >= 0 && p < a.ix.num_pages;
+        if (!good) record_status(a.status, NVFP4_ERR_PAGE);
+        int64_t at = p * page_bytes + (int64_t)(gi & ((1 << a.ix.gshift) - 1)) * kGB;
+        if (!NVFP4_IN_BOUNDS(at + kGB - 1, good ? a.ix.num_pages * page_bytes : at + kGB, a.status)) at = 0;
+        from = of_head + at;
+      }
+      there_next = __ballot_sync(0xFFFFFFFFu, good);
+    };
+    auto issue = [&](int i, int st) {  // called by the whole warp, i in order
+      if ((i & 15) == 0) look_up(i);
+      const uint32_t two = (there_next >> (2 * (i & 15))) & 3u;
+      if (two == 0) return;
+      if (lane == 0) mbar_arrive_expect_tx(&sh.bar[warp][st], (uint32_t)__popc(two) * kGB);
+      __syncwarp();
+      if ((lane >> 1) == (i & 15) && ((there_next >> lane) & 1u))
+        bulk_load(sh.ring[warp][st] + (lane & 1) * kGB, from, kGB, &sh.bar[warp][st]);
+    };
+    int ahead = 0, st_ahead = 0, st = 0;
+    for (; ahead < cnt && ahead < kStages - 1; ++ahead) {
+      issue(ahead, st_ahead++);
+      if ((ahead & 15) == 0) there = there_next;
+    }
+
     // ---- queries: B fragments of Q^T, row r = tile*kRows + 8*nt + g of the head's rows
     uint32_t qf[NT][2 * kSteps];
     float factor[NT][2];        // score units of columns 2t, 2t+1
@@ -174,43 +215,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
     }
 
-    // ---- this warp's pairs of granules j0 + 2*(warp + 8*i) and the next one
-    const int cnt = uniform(w.span.n > 0 && j1 - j0 > 2 * warp ? (j1 - j0 - 2 * warp + 2 * kAttnWarps - 1) / (2 * kAttnWarps) : 0);
-    const int gfirst = w.span.g0 + j0 + 2 * warp, gend = w.span.g0 + j1;
-    const int32_t* table = a.ix.table + (int64_t)b * a.ix.width;
-    const int64_t page_bytes = ((int64_t)a.ix.hkv << a.ix.gshift) * kGB;
-    const uint8_t* of_head = a.pages + ((int64_t)head << a.ix.gshift) * kGB;
-    // Lane x of a block of 16 pairs looks after granule x & 1 of pair x >> 1: where it lies, and whether it is there
-    // (within the span, on a page of the pool; else its tokens count as masked).
-    const uint8_t* from = nullptr;
-    uint32_t there = 0, there_next = 0;
-    auto look_up = [&](int i0) {
-      const int i = i0 + (lane >> 1), gi = gfirst + 2 * kAttnWarps * i + (lane & 1);
-      bool good = i < cnt && gi < gend && NVFP4_IN_BOUNDS(gi >> a.ix.gshift, a.ix.width, a.status);
-      if (good) {
-        const int32_t p = table[gi >> a.ix.gshift];
-        good = p >= 0 && p < a.ix.num_pages;
-        if (!good) record_status(a.status, NVFP4_ERR_PAGE);
-        int64_t at = p * page_bytes + (int64_t)(gi & ((1 << a.ix.gshift) - 1)) * kGB;
-        if (!NVFP4_IN_BOUNDS(at + kGB - 1, good ? a.ix.num_pages * page_bytes : at + kGB, a.status)) at = 0;
-        from = of_head + at;
-      }
-      there_next = __ballot_sync(0xFFFFFFFFu, good);
-    };
-    auto issue = [&](int i, int st) {  // called by the whole warp, i in order
-      if ((i & 15) == 0) look_up(i);
-      const uint32_t two = (there_next >> (2 * (i & 15))) & 3u;
-      if (two == 0) return;
-      if (lane == 0) mbar_arrive_expect_tx(&sh.bar[warp][st], (uint32_t)__popc(two) * kGB);
-      __syncwarp();
-      if ((lane >> 1) == (i & 15) && ((there_next >> lane) & 1u))
-        bulk_load(sh.ring[warp][st] + (lane & 1) * kGB, from, kGB, &sh.bar[warp][st]);
-    };
-    int ahead = 0, st_ahead = 0, st = 0;
-    for (; ahead < cnt && ahead < kStages - 1; ++ahead) {
-      issue(ahead, st_ahead++);
-      if ((ahead & 15) == 0) there = there_next;
-    }
     for (int i = 0; i < cnt; ++i) {
       if ((i & 15) == 0) there = there_next;  // the look-up of this block ran at most kStages - 1 pairs ago
       const uint32_t two = (there >> (2 * (i & 15))) & 3u;
@@ -227,11 +231,13 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       if (two == 0) continue;
 
       // S^T of 32 tokens
-      float s[NT][2][4];
+      float s[NT][2][4], s2[NT][2][4];  // two sums each: the MMAs of one would wait for one another
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) s[nt][y][0] = s[nt][y][1] = s[nt][y][2] = s[nt][y][3] = 0.0f;
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][y][e] = s2[nt][y][e] = 0.0f;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         uint32_t wa[kWords], wb[kWords];  // rows g and g + 8
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma_16816(s[nt][y], pa[0], pb[0], pa[1], pb[1], qf[nt][4 * x], qf[nt][4 * x + 1]);
-              mma_16816(s[nt][y], pa[2], pb[2], pa[3], pb[3], qf[nt][4 * x + 2], qf[nt][4 * x + 3]);
+              mma_16816(s2[nt][y], pa[2], pb[2], pa[3], pb[3], qf[nt][4 * x + 2], qf[nt][4 * x + 3]);
             }
           }
         }
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][y][e] *= factor[nt][e & 1];
+          for (int e = 0; e < 4; ++e) s[nt][y][e] = (s[nt][y][e] + s2[nt][y][e]) * factor[nt][e & 1];
       if (!whole) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -461,31 +467,31 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
         part[kRows * D + tid] = sh.m[tid];
         part[kRows * D + kRows + tid] = sh.l[tid];
       }
-      __threadfence();
       __syncthreads();
       const int64_t c0 = w.w0 / per, c1 = (w.w0 + w.n - 1) / per;  // the CTAs that share the work
-      if (tid == 0) {
-        const int last = atomicAdd(&a.counters[c0], 1) == (int)(c1 - c0);
-        if (last) a.counters[c0] = 0;  // ready for the next call
-        __threadfence();
-        sh.last = last;
-      }
+      if (tid == 0) sh.last = arrive_last(a.counters + c0, (int)(c1 - c0));
       __syncthreads();
       if (sh.last) {
-        // the parts' factors 2^(m_c - m) / l, a warp for each row, then O with eight parts' loads in flight
+        // m and l of all parts, then the factors 2^(m_c - m), then O with eight parts' loads in flight
         const int np = (int)(c1 - c0) + 1;
-        float* factor_of = &sh.join[0][0][0];  // [np][kRows]
+        float *ms = &sh.parts[0][0][0], *ls = &sh.parts[1][0][0];  // [np][kRows]; ms becomes the factors
         auto part_of = [&](int c) { return a.partial + (2 * (c0 + c) + (c == 0 ? 1 : 0)) * kPart; };
+        for (int x = tid; x < np * kRows; x += kAttnThreads) {
+          const float* p = part_of(x / kRows) + kRows * D + x % kRows;
+          ms[x] = __ldcg(p);
+          ls[x] = __ldcg(p + kRows);
+        }
+        __syncthreads();
         for (int row = warp; row < kRows; row += kAttnWarps) {
           float mt = -INFINITY, lt = 0.0f;
-          for (int c = lane; c < np; c += 32) mt = fmaxf(mt, __ldcg(part_of(c) + kRows * D + row));
+          for (int c = lane; c < np; c += 32) mt = fmaxf(mt, ms[c * kRows + row]);
 #pragma unroll
           for (int x = 16; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, x));
           for (int c = lane; c < np; c += 32) {
-            const float mc = __ldcg(part_of(c) + kRows * D + row);
+            const float mc = ms[c * kRows + row];
             const float f = mc == -INFINITY ? 0.0f : ex2(mc - mt);
-            factor_of[c * kRows + row] = f;
-            lt += f == 0.0f ? 0.0f : __ldcg(part_of(c) + kRows * D + kRows + row) * f;
+            ms[c * kRows + row] = f;
+            lt += f == 0.0f ? 0.0f : ls[c * kRows + row] * f;
           }
 #pragma unroll
           for (int x = 16; x > 0; x >>= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, x);
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
           float2 x = make_float2(0.0f, 0.0f);
 #pragma unroll 8
           for (int c = 0; c < np; ++c) {
-            const float f = factor_of[c * kRows + row];
+            const float f = ms[c * kRows + row];
             const float2 y = __ldcg(reinterpret_cast<const float2*>(part_of(c) + row * D + d));
             x.x += y.x * f;
             x.y += y.y * f;
@@ -514,7 +520,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
   }
 }
 
-constexpr int kMaxAttnCtas = 512;
 constexpr int kCounters = 512;
 constexpr int kPartFloats = 16 * (128 + 2);
 

@@ -91,6 +91,16 @@ struct AttnArgs {
 };
 
 
+// One thread's arrival, after a barrier of its CTA, at a counter of CTAs that
+// have stored their parts: true for the last of `others` + 1, which may then
+// read all of them (behind another barrier). The counter is zero again.
+NVFP4_DEVINL int arrive_last(int32_t* counter, int others) {
+  int before;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  if (before == others) *counter = 0;
+  return before == others;
+}
+
 constexpr int64_t kAttnWaitCycles = 4000000000ll;  // bound of every wait, about 2 s
 constexpr float kRescaleAt = 8.0f;                // lag of the running maximum, in log2 units
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
@@ -213,53 +223,73 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       if (kCoarse != kFine) u.coarse += __shfl_xor_sync(0xFFFFFFFFu, u.coarse, o);
     }
   };
-  if (tid == 0) sh.long_count = 0;
-  __syncthreads();
-  Two mine{0, 0};
-  for (int b = tid; b < a.ix.batch; b += kThreads) {
-    const KvSeq s = kv_sequence(a.ix, b, a.status);
-    if (tiles_of<kRows>(a, s) > kLongTiles && b < kStoredSums) {
-      const int i = atomicAdd(&sh.long_count, 1);
-      if (i < kLongList) {
-        sh.long_seq[i] = b;
-        continue;
-      }
+  const bool few = a.ix.batch <= 32;  // warp 0 alone, a lane for each sequence
+  Two own{0, 0};
+  if (few && warp == 0) {
+    KvSeq s{0, 0, 0};
+    if (lane < a.ix.batch) s = kv_sequence(a.ix, lane, a.status);
+    const bool longer = tiles_of<kRows>(a, s) > kLongTiles;
+    if (!longer) own = count(s, 0, 1);
+    for (unsigned left = __ballot_sync(0xFFFFFFFFu, longer); left; left &= left - 1) {
+      const int src = __ffs(left) - 1;
+      const KvSeq x{0, __shfl_sync(0xFFFFFFFFu, s.rows, src), __shfl_sync(0xFFFFFFFFu, s.len, src)};
+      Two u = count(x, lane, 32);
+      warp_sum(u);
+      if (lane == src) own = u;
     }
-    const Two u = count(s, 0, 1);
-    if (b < kStoredSums) {
-      sh.sums[0][b] = u.fine;
-      sh.sums[1][b] = u.coarse;
-    }
-    mine.fine += u.fine;
-    mine.coarse += u.coarse;
   }
-  __syncthreads();
-  const int longs = sh.long_count < kLongList ? sh.long_count : kLongList;
-  for (int i = warp; i < longs; i += kThreads / 32) {
-    const int b = sh.long_seq[i];
-    Two u = count(kv_sequence(a.ix, b, nullptr), lane, 32);
-    warp_sum(u);
-    if (lane == 0) {
-      sh.sums[0][b] = u.fine;
-      sh.sums[1][b] = u.coarse;
+  if (!few) {
+    if (tid == 0) sh.long_count = 0;
+    __syncthreads();
+    Two mine{0, 0};
+    for (int b = tid; b < a.ix.batch; b += kThreads) {
+      const KvSeq s = kv_sequence(a.ix, b, a.status);
+      if (tiles_of<kRows>(a, s) > kLongTiles && b < kStoredSums) {
+        const int i = atomicAdd(&sh.long_count, 1);
+        if (i < kLongList) {
+          sh.long_seq[i] = b;
+          continue;
+        }
+      }
+      const Two u = count(s, 0, 1);
+      if (b < kStoredSums) {
+        sh.sums[0][b] = u.fine;
+        sh.sums[1][b] = u.coarse;
+      }
       mine.fine += u.fine;
       mine.coarse += u.coarse;
     }
+    __syncthreads();
+    const int longs = sh.long_count < kLongList ? sh.long_count : kLongList;
+    for (int i = warp; i < longs; i += kThreads / 32) {
+      const int b = sh.long_seq[i];
+      Two u = count(kv_sequence(a.ix, b, nullptr), lane, 32);
+      warp_sum(u);
+      if (lane == 0) {
+        sh.sums[0][b] = u.fine;
+        sh.sums[1][b] = u.coarse;
+        mine.fine += u.fine;
+        mine.coarse += u.coarse;
+      }
+    }
+    warp_sum(mine);
+    if (lane == 0) {
+      sh.warp_total[0][warp] = mine.fine;
+      sh.warp_total[1][warp] = mine.coarse;
+    }
+    __syncthreads();
   }
-  warp_sum(mine);
-  if (lane == 0) {
-    sh.warp_total[0][warp] = mine.fine;
-    sh.warp_total[1][warp] = mine.coarse;
-  }
-  __syncthreads();
   if (warp == 0) {
-    Two all{0, 0};
-    if (lane < kThreads / 32) all = Two{sh.warp_total[0][lane], sh.warp_total[1][lane]};
+    Two all = own;
+    if (!few) all = lane < kThreads / 32 ? Two{sh.warp_total[0][lane], sh.warp_total[1][lane]} : Two{0, 0};
     warp_sum(all);
     const bool coarse = kCoarse != kFine && all.fine * kFine < (int64_t)gridDim.x * kCoarse;
     const int unit = coarse ? kCoarse : kFine;
     const int64_t total = coarse ? all.coarse : all.fine;
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x, u0 = per * blockIdx.x;
+    // (a 64-bit division takes as long as all the rest of this)
+    const int64_t per = total < (int64_t(1) << 31) ? ((uint32_t)total + gridDim.x - 1) / gridDim.x
+                                                   : (total + gridDim.x - 1) / gridDim.x;
+    const int64_t u0 = per * blockIdx.x;
     int64_t base = 0;
     // the lane whose part of the list, 32 values on from `base`, holds u0
     auto locate = [&](int64_t v) {
@@ -280,7 +310,9 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       for (int b0 = 0; b < 0 && b0 < a.ix.batch; b0 += 32) {
         const int x = b0 + lane;
         int64_t v = 0;
-        if (x < kStoredSums && x < a.ix.batch) {
+        if (few) {
+          v = coarse ? own.coarse : own.fine;
+        } else if (x < kStoredSums && x < a.ix.batch) {
           v = sh.sums[coarse][x];
         } else if (x < a.ix.batch) {
           const Two u = count(kv_sequence(a.ix, x, nullptr), 0, 1);
@@ -311,7 +343,7 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
         c.seq = s;
         c.span = tile_span<kRows>(a, s, tile);
         c.n = units_of(c.span, unit);
-        c.head = (int)((u0 - base) / c.n);
+        c.head = u0 - base < (int64_t(1) << 31) ? (int)(u0 - base) / c.n : (int)((u0 - base) / c.n);
         c.w0 = base + (int64_t)c.head * c.n;
       }
     }

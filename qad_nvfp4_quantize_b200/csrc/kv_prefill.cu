@@ -486,15 +486,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
               *reinterpret_cast<uint4*>(mine_p + 256 + ((8 * c + e) * 128 + row) * 4) =
                   make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
-          __threadfence();
           if (!(ok = meet())) break;
           const int64_t c0 = w.w0 / sh.part.per, c1 = (w.w0 + w.n - 1) / sh.part.per;
-          if (row == 0) {
-            const int last = atomicAdd(&a.counters[2 * c0 + i], 1) == (int)(c1 - c0);
-            if (last) a.counters[2 * c0 + i] = 0;
-            __threadfence();
-            sh.last[i] = last;
-          }
+          if (row == 0) sh.last[i] = arrive_last(a.counters + 2 * c0 + i, (int)(c1 - c0));
           if (!(ok = meet())) break;
           if (sh.last[i]) {
             float mt = -INFINITY, lt = 0.0f;
