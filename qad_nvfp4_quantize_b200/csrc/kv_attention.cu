@@ -34,9 +34,7 @@ namespace nvfp4 {
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;
-// A work is not cut into pieces of less than this many granules while CTAs are
-// left over: joining two pieces costs as long as a CTA needs for about so many.
-constexpr int kCoarseGranules = 96;
+constexpr int kLongUnit = 384;  // granules
 constexpr int kMaxAttnCtas = 320;
 
 template <int D, int NT>
@@ -96,7 +94,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
   if (tid == 0) sh.abort = 0;
   fence_barrier_init();
 
-  find_part<kRows, 1, kCoarseGranules, kAttnThreads>(a, sh.scratch, sh.part);
+  find_part<kRows, 1, kLongUnit, kAttnThreads>(a, sh.scratch, sh.part);
   const int64_t u0 = sh.part.u0, u1 = sh.part.u1, per = sh.part.per;
   if (u0 >= u1) return;
   WorkCursor<kRows> w = sh.part.cursor;
@@ -429,28 +427,32 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     __syncthreads();
 
     // ---- a whole work is written out; a part goes to the workspace, and the last part joins them
-    auto write_rows = [&](auto&& value) {  // value(row, d) = unnormalised sum; sh.m, sh.l as joined
-      for (int e = tid; e < kRows * (D / 2); e += kAttnThreads) {
-        const int row = e / (D / 2), d = (e % (D / 2)) * 2;
+    auto write_rows = [&](auto&& value) {  // value(row, d) = unnormalised sums of 4 dimensions; sh.m, sh.l as joined
+#pragma unroll
+      for (int e0 = 0; e0 < kRows * (D / 4); e0 += kAttnThreads) {
+        const int e = e0 + tid, row = e / (D / 4), d = (e % (D / 4)) * 4;
         const int32_t r = tile * kRows + row;
-        if (r >= nrows) continue;
+        if (r >= nrows || (kRows * (D / 4) < kAttnThreads && e >= kRows * (D / 4))) continue;
         const int32_t tok = r / a.group, hq = head * a.group + r - tok * a.group;
         const int64_t at = (seq.row0 + tok) * a.ix.hkv * a.group + hq;
         const float lt = sh.l[row];
         const float f = lt == 0.0f ? 0.0f : kValueScale * vg / lt;  // no visible token: zeros
-        const float2 x = value(row, d);
+        const float4 x = value(row, d);
         if (!NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status)) continue;
-        *reinterpret_cast<uint32_t*>(a.out + at * D + d) = f32x2_to_bf16x2(x.x * f, x.y * f);
+        *reinterpret_cast<uint2*>(a.out + at * D + d) =
+            make_uint2(f32x2_to_bf16x2(x.x * f, x.y * f), f32x2_to_bf16x2(x.z * f, x.w * f));
         if (a.lse && d == 0) a.lse[at] = lt == 0.0f ? -INFINITY : (sh.m[row] + log2f(lt)) * kLn2;
       }
     };
     auto joined = [&](int row, int d) {
-      float2 x = make_float2(0.0f, 0.0f);
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) {
-        const float2 y = *reinterpret_cast<const float2*>(&sh.join[w][row][d]);
+      for (int w2 = 0; w2 < kAttnWarps; ++w2) {
+        const float4 y = *reinterpret_cast<const float4*>(&sh.join[w2][row][d]);
         x.x += y.x;
         x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
       }
       return x;
     };
@@ -459,9 +461,9 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       write_rows(joined);
     } else {
       float* part = a.partial + (2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0)) * kPart;
-      for (int e = tid; e < kRows * (D / 2); e += kAttnThreads) {
-        const int row = e / (D / 2), d = (e % (D / 2)) * 2;
-        *reinterpret_cast<float2*>(part + row * D + d) = joined(row, d);
+      for (int e = tid; e < kRows * (D / 4); e += kAttnThreads) {
+        const int row = e / (D / 4), d = (e % (D / 4)) * 4;
+        *reinterpret_cast<float4*>(part + row * D + d) = joined(row, d);
       }
       if (tid < kRows) {
         part[kRows * D + tid] = sh.m[tid];
@@ -502,13 +504,16 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
         }
         __syncthreads();
         write_rows([&](int row, int d) {
-          float2 x = make_float2(0.0f, 0.0f);
-#pragma unroll 8
+          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          const float* p = part_of(0) + row * D + d;  // the later parts lie 2 * kPart apart, the first one kPart behind
+#pragma unroll 16
           for (int c = 0; c < np; ++c) {
             const float f = ms[c * kRows + row];
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(part_of(c) + row * D + d));
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + (c == 0 ? 0 : (2 * c - 1) * kPart)));
             x.x += y.x * f;
             x.y += y.y * f;
+            x.z += y.z * f;
+            x.w += y.w * f;
           }
           return x;
         });

@@ -190,50 +190,65 @@ struct Part {
   int64_t u0, u1, per;  // this CTA's units [u0, u1); units of a CTA
 };
 struct PartScratch {
-  int64_t sums[2][kStoredSums];
-  int64_t warp_total[2][32];
+  int64_t sums[3][kStoredSums];
+  int64_t warp_total[3][32];
   int32_t long_seq[kLongList];
   int32_t long_count;
 };
 
-// This CTA's part of the list, called by all kThreads threads. Units are kFine
-// granules, or kCoarse where that leaves less than kCoarse granules to a CTA:
-// then works are not cut into smaller pieces than that (kCoarse a multiple of
-// kFine). A thread counts a sequence, a warp one of many tiles.
-template <int kRows, int kFine, int kCoarse, int kThreads>
+// This CTA's part of the list, called by all kThreads threads. A unit is kFine
+// granules, so that all parts are equal, or a longer run (at most kLong
+// granules, then whole works mostly), so that fewer works are cut: a piece costs
+// its queries, its pipeline's start and the warps' meeting, a cut one the joining
+// as well. Which is chosen by the granules that a CTA would take and those that
+// these costs are worth (kPieceCost, kCutCost, measured). With kLong = kFine
+// there is no choice. A thread counts a sequence, a warp one of many tiles.
+constexpr int kPieceCost = 40, kCutCost = 50;
+
+template <int kRows, int kFine, int kLong, int kThreads>
 NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& part) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  struct Two {
-    int64_t fine, coarse;
+  constexpr int kMid = kLong == kFine ? kFine : kLong / 4;
+  constexpr int kKinds = kLong == kFine ? 1 : 3;
+  constexpr int kUnit[3] = {kFine, kMid, kLong};
+  struct Sums {
+    int64_t of[kKinds];
   };
   auto count = [&](const KvSeq& s, int t0, int step) {
-    Two u{0, 0};
+    Sums u{};
     const int tiles = tiles_of<kRows>(a, s);
     for (int t = t0; t < tiles; t += step) {
       const Span span = tile_span<kRows>(a, s, t);
-      u.fine += units_of(span, kFine);
-      u.coarse += units_of(span, kCoarse);
-    }
-    return Two{u.fine * a.ix.hkv, u.coarse * a.ix.hkv};
-  };
-  auto warp_sum = [&](Two& u) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      u.fine += __shfl_xor_sync(0xFFFFFFFFu, u.fine, o);
-      if (kCoarse != kFine) u.coarse += __shfl_xor_sync(0xFFFFFFFFu, u.coarse, o);
+      for (int k = 0; k < kKinds; ++k) u.of[k] += (int64_t)units_of(span, kUnit[k]) * a.ix.hkv;
     }
+    return u;
+  };
+  auto warp_sum = [&](Sums& u) {
+    bool small = true;  // 32 summands below 2^26
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k) small = small && u.of[k] < (1 << 26);
+    if (__all_sync(0xFFFFFFFFu, small)) {
+#pragma unroll
+      for (int k = 0; k < kKinds; ++k) u.of[k] = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)u.of[k]);
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) u.of[k] += __shfl_xor_sync(0xFFFFFFFFu, u.of[k], o);
   };
   const bool few = a.ix.batch <= 32;  // warp 0 alone, a lane for each sequence
-  Two own{0, 0};
+  Sums own{};
+  KvSeq mine{0, 0, 0};
   if (few && warp == 0) {
-    KvSeq s{0, 0, 0};
-    if (lane < a.ix.batch) s = kv_sequence(a.ix, lane, a.status);
-    const bool longer = tiles_of<kRows>(a, s) > kLongTiles;
-    if (!longer) own = count(s, 0, 1);
+    if (lane < a.ix.batch) mine = kv_sequence(a.ix, lane, a.status);
+    const bool longer = tiles_of<kRows>(a, mine) > kLongTiles;
+    if (!longer) own = count(mine, 0, 1);
     for (unsigned left = __ballot_sync(0xFFFFFFFFu, longer); left; left &= left - 1) {
       const int src = __ffs(left) - 1;
-      const KvSeq x{0, __shfl_sync(0xFFFFFFFFu, s.rows, src), __shfl_sync(0xFFFFFFFFu, s.len, src)};
-      Two u = count(x, lane, 32);
+      const KvSeq x{0, __shfl_sync(0xFFFFFFFFu, mine.rows, src), __shfl_sync(0xFFFFFFFFu, mine.len, src)};
+      Sums u = count(x, lane, 32);
       warp_sum(u);
       if (lane == src) own = u;
     }
@@ -241,7 +256,7 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
   if (!few) {
     if (tid == 0) sh.long_count = 0;
     __syncthreads();
-    Two mine{0, 0};
+    Sums sum{};
     for (int b = tid; b < a.ix.batch; b += kThreads) {
       const KvSeq s = kv_sequence(a.ix, b, a.status);
       if (tiles_of<kRows>(a, s) > kLongTiles && b < kStoredSums) {
@@ -251,45 +266,60 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
           continue;
         }
       }
-      const Two u = count(s, 0, 1);
-      if (b < kStoredSums) {
-        sh.sums[0][b] = u.fine;
-        sh.sums[1][b] = u.coarse;
+      const Sums u = count(s, 0, 1);
+#pragma unroll
+      for (int k = 0; k < kKinds; ++k) {
+        if (b < kStoredSums) sh.sums[k][b] = u.of[k];
+        sum.of[k] += u.of[k];
       }
-      mine.fine += u.fine;
-      mine.coarse += u.coarse;
     }
     __syncthreads();
     const int longs = sh.long_count < kLongList ? sh.long_count : kLongList;
     for (int i = warp; i < longs; i += kThreads / 32) {
       const int b = sh.long_seq[i];
-      Two u = count(kv_sequence(a.ix, b, nullptr), lane, 32);
+      Sums u = count(kv_sequence(a.ix, b, nullptr), lane, 32);
       warp_sum(u);
-      if (lane == 0) {
-        sh.sums[0][b] = u.fine;
-        sh.sums[1][b] = u.coarse;
-        mine.fine += u.fine;
-        mine.coarse += u.coarse;
-      }
+      if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < kKinds; ++k) {
+          sh.sums[k][b] = u.of[k];
+          sum.of[k] += u.of[k];
+        }
     }
-    warp_sum(mine);
-    if (lane == 0) {
-      sh.warp_total[0][warp] = mine.fine;
-      sh.warp_total[1][warp] = mine.coarse;
-    }
+    warp_sum(sum);
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < kKinds; ++k) sh.warp_total[k][warp] = sum.of[k];
     __syncthreads();
   }
   if (warp == 0) {
-    Two all = own;
-    if (!few) all = lane < kThreads / 32 ? Two{sh.warp_total[0][lane], sh.warp_total[1][lane]} : Two{0, 0};
+    Sums all = own;
+    if (!few)
+#pragma unroll
+      for (int k = 0; k < kKinds; ++k) all.of[k] = lane < kThreads / 32 ? sh.warp_total[k][lane] : 0;
     warp_sum(all);
-    const bool coarse = kCoarse != kFine && all.fine * kFine < (int64_t)gridDim.x * kCoarse;
-    const int unit = coarse ? kCoarse : kFine;
-    const int64_t total = coarse ? all.coarse : all.fine;
     // (a 64-bit division takes as long as all the rest of this)
-    const int64_t per = total < (int64_t(1) << 31) ? ((uint32_t)total + gridDim.x - 1) / gridDim.x
-                                                   : (total + gridDim.x - 1) / gridDim.x;
-    const int64_t u0 = per * blockIdx.x;
+    auto parts = [&](int64_t total) {
+      return total < (int64_t(1) << 31) ? (int64_t)(((uint32_t)total + gridDim.x - 1) / gridDim.x)
+                                        : (total + gridDim.x - 1) / gridDim.x;
+    };
+    int kind = 0;
+    if (kKinds > 1) {
+      float best = (float)parts(all.of[0]) + 2 * (kPieceCost + kCutCost);
+#pragma unroll
+      for (int k = 1; k < kKinds; ++k) {
+        const bool cut = k < kKinds - 1 && all.of[k] > all.of[kKinds - 1];
+        const float takes = (float)parts(all.of[k]) *
+                            (1.125f * (float)all.of[0] / (float)all.of[k] + kPieceCost + (cut ? kCutCost : 0));
+        if (takes < best) {
+          best = takes;
+          kind = k;
+        }
+      }
+    }
+    const int unit = kind == 0 ? kFine : kind == 1 ? kMid : kLong;
+    const int64_t total = kind == 0 ? all.of[0] : kind == 1 ? all.of[1 % kKinds] : all.of[2 % kKinds];
+    const int64_t per = parts(total), u0 = per * blockIdx.x;
     int64_t base = 0;
     // the lane whose part of the list, 32 values on from `base`, holds u0
     auto locate = [&](int64_t v) {
@@ -304,24 +334,30 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       base += __shfl_sync(0xFFFFFFFFu, at ? incl - v : incl, src);
       return at ? src : -1;
     };
+    auto of_kind = [&](const Sums& u) { return kind == 0 ? u.of[0] : kind == 1 ? u.of[1 % kKinds] : u.of[2 % kKinds]; };
     int b = -1, tile = -1;
     KvSeq s{0, 0, 0};
     if (u0 < total) {
-      for (int b0 = 0; b < 0 && b0 < a.ix.batch; b0 += 32) {
-        const int x = b0 + lane;
-        int64_t v = 0;
-        if (few) {
-          v = coarse ? own.coarse : own.fine;
-        } else if (x < kStoredSums && x < a.ix.batch) {
-          v = sh.sums[coarse][x];
-        } else if (x < a.ix.batch) {
-          const Two u = count(kv_sequence(a.ix, x, nullptr), 0, 1);
-          v = coarse ? u.coarse : u.fine;
+      if (few) {
+        b = locate(of_kind(own));
+        if (b >= 0) {
+          s.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, b);
+          s.rows = __shfl_sync(0xFFFFFFFFu, mine.rows, b);
+          s.len = __shfl_sync(0xFFFFFFFFu, mine.len, b);
         }
-        const int src = locate(v);
-        if (src >= 0) b = b0 + src;
+      } else {
+        for (int b0 = 0; b < 0 && b0 < a.ix.batch; b0 += 32) {
+          const int x = b0 + lane;
+          int64_t v = 0;
+          if (x < kStoredSums && x < a.ix.batch)
+            v = sh.sums[kind][x];
+          else if (x < a.ix.batch)
+            v = of_kind(count(kv_sequence(a.ix, x, nullptr), 0, 1));
+          const int src = locate(v);
+          if (src >= 0) b = b0 + src;
+        }
+        if (b >= 0) s = kv_sequence(a.ix, b, nullptr);
       }
-      if (b >= 0) s = kv_sequence(a.ix, b, nullptr);
       const int tiles = tiles_of<kRows>(a, s);
       if (tiles == 1) tile = 0;
       for (int t0 = 0; tile < 0 && t0 < tiles; t0 += 32) {
