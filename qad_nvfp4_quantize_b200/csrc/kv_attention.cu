@@ -34,7 +34,7 @@ namespace nvfp4 {
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kLongUnit = 384;  // granules
+constexpr int kLongUnit = 384, kHeadUnits = 60;  // granules
 constexpr int kMaxAttnCtas = 320;
 
 template <int D, int NT>
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
   if (tid == 0) sh.abort = 0;
   fence_barrier_init();
 
-  find_part<kRows, 1, kLongUnit, kAttnThreads>(a, sh.scratch, sh.part);
+  find_part<kRows, 1, kLongUnit, kHeadUnits, kAttnThreads>(a, sh.scratch, sh.part);
   const int64_t u0 = sh.part.u0, u1 = sh.part.u1, per = sh.part.per;
   if (u0 >= u1) return;
   WorkCursor<kRows> w = sh.part.cursor;
@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     u = w.w0 + unit1;
     const KvSeq& seq = w.seq;
     const int tile = w.tile, head = w.head, b = w.b;
-    const int j0 = unit0 * w.unit, j1 = unit1 * w.unit < w.span.n ? unit1 * w.unit : w.span.n;  // granules
+    int j0, j1;  // granules
+    w.granules(unit0, unit1, j0, j1);
 
     // ---- this warp's pairs of granules j0 + 2*(warp + 8*i) and the next one; the first ones are fetched while the
     // queries are prepared

@@ -129,7 +129,8 @@ NVFP4_DEVINL bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abo
 // ---------------------------------------------------------------------------
 // Work list. A work is one KV head of one tile of kRows query rows of one
 // sequence (row r = new token r / group, query head r % group of the KV head);
-// its units are runs of `unit` granules that some row of the tile sees, at least
+// its units are runs of `unit` granules that some row of the tile sees, after
+// `head_units` that stand for what a work costs besides its granules; at least
 // one (a tile that sees nothing still writes its rows). The works of a launch
 // in order (sequence, tile, head) and their units form one list, from which
 // every CTA takes an equal part: the lengths are read on the device, so ragged
@@ -153,7 +154,9 @@ template <int kRows>
 NVFP4_DEVINL int tiles_of(const AttnArgs& a, const KvSeq& s) {
   return (s.rows * a.group + (kRows - 1)) / kRows;
 }
-NVFP4_DEVINL int units_of(const Span& s, int unit) { return s.n > unit ? (s.n + unit - 1) / unit : 1; }
+NVFP4_DEVINL int units_of(const Span& s, int unit, int head_units) {
+  return head_units + (s.n > unit ? (s.n + unit - 1) / unit : 1);
+}
 
 constexpr int kStoredSums = 256, kLongList = 64, kLongTiles = 16;
 
@@ -164,7 +167,7 @@ struct WorkCursor {
   Span span;
   int b, tile, head, n;  // n: units of the work
   int64_t w0;            // the work's first unit
-  int unit;
+  int unit, head_units;
   NVFP4_DEVINL bool next(const AttnArgs& a) {  // false behind the last work
     w0 += n;
     if (++head < a.ix.hkv) return true;
@@ -177,8 +180,15 @@ struct WorkCursor {
       } while (seq.rows == 0);
     }
     span = tile_span<kRows>(a, seq, tile);
-    n = units_of(span, unit);
+    n = units_of(span, unit, head_units);
     return true;
+  }
+  // Granules of the work's units [first, last).
+  NVFP4_DEVINL void granules(int first, int last, int& g0, int& g1) const {
+    g0 = (first < head_units ? 0 : first - head_units) * unit;
+    g1 = (last < head_units ? 0 : last - head_units) * unit;
+    if (g0 > span.n) g0 = span.n;
+    if (g1 > span.n) g1 = span.n;
   }
 };
 
@@ -190,29 +200,33 @@ struct Part {
   int64_t u0, u1, per;  // this CTA's units [u0, u1); units of a CTA
 };
 struct PartScratch {
-  int64_t sums[3][kStoredSums];
-  int64_t warp_total[3][32];
+  int64_t sums[4][kStoredSums];
+  int64_t warp_total[4][32];
   int32_t long_seq[kLongList];
   int32_t long_count;
 };
 
-// This CTA's part of the list, called by all kThreads threads. A unit is kFine
-// granules, so that all parts are equal, or a longer run (at most kLong
-// granules, then whole works mostly), so that fewer works are cut: a piece costs
-// its queries, its pipeline's start and the warps' meeting, a cut one the joining
-// as well. Which is chosen by the granules that a CTA would take and those that
-// these costs are worth (kPieceCost, kCutCost, measured). With kLong = kFine
-// there is no choice. A thread counts a sequence, a warp one of many tiles.
-constexpr int kPieceCost = 40, kCutCost = 50;
-
-template <int kRows, int kFine, int kLong, int kThreads>
+// This CTA's part of the list, called by all kThreads threads. What a piece of a
+// work costs besides its granules (its queries, its pipeline's start, the warps'
+// meeting) is worth kHead units of kFine granules, and joining the pieces of a
+// cut work about as much again (measured); so units are chosen among
+//   kFine granules and kHead in front of a work: all CTAs take equally much;
+//   runs of kLong / 4 or kLong granules: short works are not cut;
+//   the longest run of which every CTA gets one, if there are few works: no CTA
+//   has the end of one work and the start of another.
+// With kLong = kFine the first is taken. A thread counts a sequence, a warp one
+// of many tiles.
+template <int kRows, int kFine, int kLong, int kHead, int kThreads>
 NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& part) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kMid = kLong == kFine ? kFine : kLong / 4;
   constexpr int kKinds = kLong == kFine ? 1 : 3;
   constexpr int kUnit[3] = {kFine, kMid, kLong};
+  constexpr int kHeads[3] = {kHead, 0, 0};
+  constexpr float kPieceCost = kHead, kCutCost = 1.5f * kHead;  // and one for each piece that is joined
+  constexpr int kSums = kKinds + 1;  // the units of each kind, and the works
   struct Sums {
-    int64_t of[kKinds];
+    int64_t of[kSums];
   };
   auto count = [&](const KvSeq& s, int t0, int step) {
     Sums u{};
@@ -220,21 +234,22 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
     for (int t = t0; t < tiles; t += step) {
       const Span span = tile_span<kRows>(a, s, t);
 #pragma unroll
-      for (int k = 0; k < kKinds; ++k) u.of[k] += (int64_t)units_of(span, kUnit[k]) * a.ix.hkv;
+      for (int k = 0; k < kKinds; ++k) u.of[k] += (int64_t)units_of(span, kUnit[k], kHeads[k]) * a.ix.hkv;
+      u.of[kKinds] += a.ix.hkv;
     }
     return u;
   };
   auto warp_sum = [&](Sums& u) {
     bool small = true;  // 32 summands below 2^26
 #pragma unroll
-    for (int k = 0; k < kKinds; ++k) small = small && u.of[k] < (1 << 26);
+    for (int k = 0; k < kSums; ++k) small = small && u.of[k] < (1 << 26);
     if (__all_sync(0xFFFFFFFFu, small)) {
 #pragma unroll
-      for (int k = 0; k < kKinds; ++k) u.of[k] = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)u.of[k]);
+      for (int k = 0; k < kSums; ++k) u.of[k] = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)u.of[k]);
       return;
     }
 #pragma unroll
-    for (int k = 0; k < kKinds; ++k)
+    for (int k = 0; k < kSums; ++k)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) u.of[k] += __shfl_xor_sync(0xFFFFFFFFu, u.of[k], o);
   };
@@ -268,7 +283,7 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       }
       const Sums u = count(s, 0, 1);
 #pragma unroll
-      for (int k = 0; k < kKinds; ++k) {
+      for (int k = 0; k < kSums; ++k) {
         if (b < kStoredSums) sh.sums[k][b] = u.of[k];
         sum.of[k] += u.of[k];
       }
@@ -281,7 +296,7 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       warp_sum(u);
       if (lane == 0)
 #pragma unroll
-        for (int k = 0; k < kKinds; ++k) {
+        for (int k = 0; k < kSums; ++k) {
           sh.sums[k][b] = u.of[k];
           sum.of[k] += u.of[k];
         }
@@ -289,36 +304,57 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
     warp_sum(sum);
     if (lane == 0)
 #pragma unroll
-      for (int k = 0; k < kKinds; ++k) sh.warp_total[k][warp] = sum.of[k];
+      for (int k = 0; k < kSums; ++k) sh.warp_total[k][warp] = sum.of[k];
     __syncthreads();
   }
   if (warp == 0) {
     Sums all = own;
     if (!few)
 #pragma unroll
-      for (int k = 0; k < kKinds; ++k) all.of[k] = lane < kThreads / 32 ? sh.warp_total[k][lane] : 0;
+      for (int k = 0; k < kSums; ++k) all.of[k] = lane < kThreads / 32 ? sh.warp_total[k][lane] : 0;
     warp_sum(all);
     // (a 64-bit division takes as long as all the rest of this)
     auto parts = [&](int64_t total) {
       return total < (int64_t(1) << 31) ? (int64_t)(((uint32_t)total + gridDim.x - 1) / gridDim.x)
                                         : (total + gridDim.x - 1) / gridDim.x;
     };
-    int kind = 0;
+    int kind = 0, unit = kFine, head_units = kHead;
+    int64_t total = all.of[0];
     if (kKinds > 1) {
-      float best = (float)parts(all.of[0]) + 2 * (kPieceCost + kCutCost);
+      const int64_t works = all.of[kKinds];
+      const float granules = fmaxf((float)(all.of[0] - works * kHead), 1.0f);
+      float best = (float)parts(all.of[0]) + kPieceCost + kCutCost;
 #pragma unroll
       for (int k = 1; k < kKinds; ++k) {
-        const bool cut = k < kKinds - 1 && all.of[k] > all.of[kKinds - 1];
-        const float takes = (float)parts(all.of[k]) *
-                            (1.125f * (float)all.of[0] / (float)all.of[k] + kPieceCost + (cut ? kCutCost : 0));
+        const bool cut = all.of[k] > works;
+        const float takes = (float)parts(all.of[k]) * (1.125f * granules / (float)all.of[k] + kPieceCost +
+                                                       (cut ? kCutCost + (float)all.of[k] / (float)works : 0.0f));
         if (takes < best) {
           best = takes;
           kind = k;
         }
       }
+      if (few && 2 * works <= gridDim.x) {  // ceil(n / unit) over the works is at most granules / unit + works
+        const int run = (int)ceilf(granules / (float)((int)gridDim.x - (int)works)) + 1;
+        const float takes = (float)run + kPieceCost + kCutCost + granules / (float)run / (float)works;
+        if (takes < best) kind = 3, unit = run;
+      }
+      if (kind) {
+        if (kind < 3) unit = kind == 1 ? kMid : kLong;
+        head_units = 0;
+        if (kind < 3) {
+          total = kind == 1 ? all.of[1 % kKinds] : all.of[2 % kKinds];
+        } else {
+          int64_t u = 0;
+          for (int t = 0; t < tiles_of<kRows>(a, mine); ++t)
+            u += (int64_t)units_of(tile_span<kRows>(a, mine, t), unit, 0) * a.ix.hkv;
+          own.of[0] = u;
+          Sums again = own;
+          warp_sum(again);
+          total = again.of[0];
+        }
+      }
     }
-    const int unit = kind == 0 ? kFine : kind == 1 ? kMid : kLong;
-    const int64_t total = kind == 0 ? all.of[0] : kind == 1 ? all.of[1 % kKinds] : all.of[2 % kKinds];
     const int64_t per = parts(total), u0 = per * blockIdx.x;
     int64_t base = 0;
     // the lane whose part of the list, 32 values on from `base`, holds u0
@@ -334,7 +370,7 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       base += __shfl_sync(0xFFFFFFFFu, at ? incl - v : incl, src);
       return at ? src : -1;
     };
-    auto of_kind = [&](const Sums& u) { return kind == 0 ? u.of[0] : kind == 1 ? u.of[1 % kKinds] : u.of[2 % kKinds]; };
+    auto of_kind = [&](const Sums& u) { return kind == 1 ? u.of[1 % kKinds] : kind == 2 ? u.of[2 % kKinds] : u.of[0]; };
     int b = -1, tile = -1;
     KvSeq s{0, 0, 0};
     if (u0 < total) {
@@ -362,13 +398,14 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       if (tiles == 1) tile = 0;
       for (int t0 = 0; tile < 0 && t0 < tiles; t0 += 32) {
         const int x = t0 + lane;
-        const int src = locate(x < tiles ? (int64_t)units_of(tile_span<kRows>(a, s, x), unit) * a.ix.hkv : 0);
+        const int src = locate(x < tiles ? (int64_t)units_of(tile_span<kRows>(a, s, x), unit, head_units) * a.ix.hkv : 0);
         if (src >= 0) tile = t0 + src;
       }
     }
     if (lane == 0) {
       WorkCursor<kRows>& c = part.cursor;
       c.unit = unit;
+      c.head_units = head_units;
       part.per = per;
       part.u0 = u0;
       // (no tile: the lengths changed under way, from another stream; no work rather than a wrong one)
@@ -378,7 +415,7 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
         c.tile = tile;
         c.seq = s;
         c.span = tile_span<kRows>(a, s, tile);
-        c.n = units_of(c.span, unit);
+        c.n = units_of(c.span, unit, head_units);
         c.head = u0 - base < (int64_t(1) << 31) ? (int)(u0 - base) / c.n : (int)((u0 - base) / c.n);
         c.w0 = base + (int64_t)c.head * c.n;
       }

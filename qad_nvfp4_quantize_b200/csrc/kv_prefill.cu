@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     sh.abort = 0;
     fence_barrier_init();
   }
-  find_part<kPreRows, kUnitGranules, kUnitGranules, kPreThreads>(a, sh.scratch, sh.part);
+  find_part<kPreRows, kUnitGranules, kUnitGranules, 0, kPreThreads>(a, sh.scratch, sh.part);
   if (sh.part.u0 >= sh.part.u1) return;
   const int64_t u0 = sh.part.u0;
   WorkCursor<kPreRows>& w = sh.cursor[warp];
