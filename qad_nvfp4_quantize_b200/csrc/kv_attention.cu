@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       for (int c = 0; c < 2; ++c) {
         const int32_t rc = tile * kRows + 8 * nt + 2 * t + c;
         const int ec = __shfl_sync(0xFFFFFFFFu, ex, (2 * t + c) * 4);
-        factor[nt][c] = scale_exp2(a.scale * kg * kLog2e, kValueExp - ec);
+        // not zero: a masked score is -Inf before it is multiplied
+        factor[nt][c] = fmaxf(scale_exp2(a.scale * kg * kLog2e, kValueExp - ec), 1.17549435e-38f);
         Visible v{0, 0};
         if (rc < nrows) v = visible(seq.len - seq.rows + rc / a.group, seq.len, a.causal, a.window);
         lo[nt][c] = v.lo;
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     float m[NT][2], l[NT][2], o[NT][kSteps][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kStartMax;
       l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
@@ -230,13 +231,13 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       if (two == 0) continue;
 
       // S^T of 32 tokens
-      float s[NT][2][4], s2[NT][2][4];  // two sums each: the MMAs of one would wait for one another
+      float s[NT][2][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][y][e] = s2[nt][y][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) s[nt][y][e] = 0.0f;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         uint32_t wa[kWords], wb[kWords];  // rows g and g + 8
@@ -275,22 +276,16 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma_16816(s[nt][y], pa[0], pb[0], pa[1], pb[1], qf[nt][4 * x], qf[nt][4 * x + 1]);
-              mma_16816(s2[nt][y], pa[2], pb[2], pa[3], pb[3], qf[nt][4 * x + 2], qf[nt][4 * x + 3]);
+              mma_16816(s[nt][y], pa[2], pb[2], pa[3], pb[3], qf[nt][4 * x + 2], qf[nt][4 * x + 3]);
             }
           }
         }
       }
 
-      // scores in log2 units, mask, running maximum
+      // mask, running maximum (m in log2 units; scores become that with the row's factor in the exponent's FMA)
       const int tok0 = (gfirst + 2 * kAttnWarps * i) * kGranule;
       const bool whole = tok0 >= all_lo && tok0 + 2 * kGranule <= all_hi && two == 3u;
       bool grow = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][y][e] = (s[nt][y][e] + s2[nt][y][e]) * factor[nt][e & 1];
       if (!whole) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -302,22 +297,25 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
               if (tk < lo[nt][c] || tk >= hi[nt][c] || !((two >> y) & 1u)) s[nt][y][e] = -INFINITY;
             }
       }
+      float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          grow |= fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2])) > m[nt][c] + kRescaleAt;
+        for (int c = 0; c < 2; ++c) {
+          top[nt][c] = fmaxf(max3(s[nt][0][c], s[nt][0][c + 2], s[nt][1][c]), s[nt][1][c + 2]) * factor[nt][c];
+          grow |= top[nt][c] > m[nt][c] + kRescaleAt;
+        }
       if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2]));
+            float mx = top[nt][c];
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
             const float m1 = fmaxf(m[nt][c], mx);
-            const float f = m[nt][c] == -INFINITY ? 0.0f : ex2(m[nt][c] - m1);
+            const float f = m[nt][c] == kStartMax ? 0.0f : ex2(m[nt][c] - m1);
             m[nt][c] = m1;
             l[nt][c] *= f;
 #pragma unroll
@@ -331,15 +329,15 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
       uint32_t pf[NT][2][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float p0 = ex2(s[nt][y][0] - m0), p1 = ex2(s[nt][y][1] - m1);
-          const float p2 = ex2(s[nt][y][2] - m0), p3 = ex2(s[nt][y][3] - m1);
-          l[nt][0] += p0 + p2;
-          l[nt][1] += p1 + p3;
-          pf[nt][y][0] = transpose_8x8(half2_bits(p0, p1));
-          pf[nt][y][1] = transpose_8x8(half2_bits(p2, p3));
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = ex2(__fmaf_rn(s[nt][y][e], factor[nt][e & 1], -m[nt][e & 1]));
+          l[nt][0] += p[0] + p[2];
+          l[nt][1] += p[1] + p[3];
+          pf[nt][y][0] = transpose_8x8(half2_bits(p[0], p[1]));
+          pf[nt][y][1] = transpose_8x8(half2_bits(p[2], p[3]));
         }
       }
 
@@ -389,6 +387,11 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_ke
     }
 
     // ---- the warps' parts meet
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (m[nt][c] == kStartMax) m[nt][c] = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -47,6 +47,12 @@ NVFP4_DEVINL float ex2(float x) {
   return r;
 }
 
+NVFP4_DEVINL float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Power of two that brings a row of BF16 queries whose largest magnitude is
 // amax to [2^14, 2^15), as the exponent to add (0 for a zero or non-finite
 // row). FP16 then holds every query exactly down to 2^-29 of the row's largest,
@@ -103,6 +109,7 @@ NVFP4_DEVINL int arrive_last(int32_t* counter, int others) {
 
 constexpr int64_t kAttnWaitCycles = 4000000000ll;  // bound of every wait, about 2 s
 constexpr float kRescaleAt = 8.0f;                // lag of the running maximum, in log2 units
+constexpr float kStartMax = -1e30f;                // running maximum before the first visible token
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 // The same value in every lane, in a form that the compiler knows to be uniform.

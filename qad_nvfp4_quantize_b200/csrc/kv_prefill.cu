@@ -41,7 +41,6 @@ constexpr int kUnitGranules = kTileTokens / kGranule;
 // Of every six pairs of weights one comes from the FMA pipe instead of the 2^x unit. Measured, 4,096 over 12,288: none
 // 673 us, one of eight 660, of six 651, of four 684, of two 751.
 constexpr int kPolyEvery = 6;
-constexpr float kStartMax = -1e30f;  // m before the first visible token, in log2 units
 
 template <int D>
 struct PreShared {
@@ -183,11 +182,6 @@ NVFP4_DEVINL void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
       : "memory");
 }
 NVFP4_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-NVFP4_DEVINL float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 NVFP4_DEVINL f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
