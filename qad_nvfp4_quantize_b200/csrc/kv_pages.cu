@@ -45,6 +45,7 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* sh, int* total) 
 // by HBM (each byte read and written once). One 256-thread CTA copies pieces
 // of 16 KB, four 16-byte loads in flight per thread; an entry is as many
 // pieces as its page needs, so a few large pages spread over the card too.
+constexpr int kRowThreads = 256;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPiece = kCopyThreads * 4;  // 16-byte vectors
 
@@ -101,6 +102,22 @@ NVFP4_DEVINL int32_t slot_len(const PoolIndex& p, int32_t slot, int* status) {
   return (int32_t)(len < 0 ? 0 : len > most ? most : len);
 }
 
+// Entry j of child i's row of the table: a shared page counted once more, or the
+// part page's copy.
+NVFP4_DEVINL void fork_entry(const PoolIndex& p, int a, int c, int to, int64_t j, int* status) {
+  const int64_t full = p.seq_len[c] / p.page;
+  if (j < full) {
+    const int64_t page = p.table[(int64_t)a * p.width + j];
+    p.table[(int64_t)c * p.width + j] = (int32_t)page;
+    if (page < 0 || page >= p.num_pages)
+      record_status(status, NVFP4_ERR_PAGE);
+    else
+      atomicAdd(&p.refs[page], 1);
+  } else if (j == full && to >= 0) {
+    p.table[(int64_t)c * p.width + j] = to;
+  }
+}
+
 // One CTA: which entries are sound, which pages the part pages are copied to.
 // src[i], dst[i] = the part page and its copy, -1 where the parent ends with a
 // full page, -2 where the entry is refused (a slot out of range, a child that
@@ -109,7 +126,8 @@ NVFP4_DEVINL int32_t slot_len(const PoolIndex& p, int32_t slot, int* status) {
 // reference counts 16 to a thread and stops at the last one needed.
 __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(PoolIndex p, const int32_t* __restrict__ parent,
                                                                     const int32_t* __restrict__ child, int n,
-                                                                    int32_t* src, int32_t* dst, int* status) {
+                                                                    int32_t* src, int32_t* dst, int with_rows,
+                                                                    int* status) {
   __shared__ int sh[kPlanWarps + 1];
   const int t = threadIdx.x;
   // dst[i] holds the parent's length until its page is known
@@ -153,9 +171,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(PoolIndex p,
   for (int64_t p0 = 0; p0 < p.num_pages && found < need; p0 += 16 * kPlanThreads) {
     const int64_t at = p0 + 16 * t;
     uint32_t mask = 0;
+    if (at + 16 <= p.num_pages && (reinterpret_cast<uintptr_t>(p.refs) & 15u) == 0) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (at + e < p.num_pages && p.refs[at + e] == 0) mask |= 1u << e;
+      for (int e = 0; e < 4; ++e) {
+        const int4 r = *reinterpret_cast<const int4*>(p.refs + at + 4 * e);
+        mask |= (uint32_t)((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << (4 * e);
+      }
+    } else {
+      for (int e = 0; e < 16; ++e)
+        if (at + e < p.num_pages && p.refs[at + e] == 0) mask |= 1u << e;
+    }
     int sum;
     int r = found + block_exclusive_scan(__popc(mask), sh, &sum);
     found += sum;
@@ -189,31 +214,25 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(PoolIndex p,
     }
     __syncthreads();
   }
+  if (!with_rows) return;
+  for (int64_t e = t; e < (int64_t)n * p.width; e += kPlanThreads) {
+    const int i = (int)(e / p.width);
+    if (dst[i] != -2) fork_entry(p, parent[i], child[i], dst[i], e - (int64_t)i * p.width, status);
+  }
 }
 
-// The children's rows of the table: shared pages counted once more, then the
-// part page's copy. Bound by the atomics' latency; a CTA for each 256 entries
-// of a row.
-constexpr int kRowThreads = 256;
+// A small fork's rows are written by the planning CTA itself: one launch less
+// (3 us of host time, 2 us on the device) for up to this many entries.
+constexpr int64_t kForkRowsInPlan = 4 * kPlanThreads;
+
+// The children's rows of the table, a CTA for each 256 entries. Bound by the
+// atomics' latency.
 __global__ void __launch_bounds__(kRowThreads) kv_fork_rows_kernel(PoolIndex p, const int32_t* __restrict__ parent,
                                                                    const int32_t* __restrict__ child,
                                                                    const int32_t* __restrict__ dst, int* status) {
-  const int i = blockIdx.x;
-  const int to = dst[i];
+  const int i = blockIdx.x, to = dst[i];
   if (to == -2) return;
-  const int a = parent[i], c = child[i];
-  const int64_t full = p.seq_len[c] / p.page;
-  const int64_t j = (int64_t)blockIdx.y * kRowThreads + threadIdx.x;
-  if (j < full) {
-    const int64_t page = p.table[(int64_t)a * p.width + j];
-    p.table[(int64_t)c * p.width + j] = (int32_t)page;
-    if (page < 0 || page >= p.num_pages)
-      record_status(status, NVFP4_ERR_PAGE);
-    else
-      atomicAdd(&p.refs[page], 1);
-  } else if (j == full && to >= 0) {
-    p.table[(int64_t)c * p.width + j] = to;
-  }
+  fork_entry(p, parent[i], child[i], to, (int64_t)blockIdx.y * kRowThreads + threadIdx.x, status);
 }
 
 cudaError_t launch_kv_fork(const PoolArgs& a, const int32_t* parent, const int32_t* child, int n, int32_t* src,
@@ -221,9 +240,10 @@ cudaError_t launch_kv_fork(const PoolArgs& a, const int32_t* parent, const int32
   if (n == 0) return cudaSuccess;
   const PoolIndex p{a.refs, a.table, a.seq_len, a.num_pages, a.slots, a.width, a.page};
   note_launch();
-  kv_fork_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, parent, child, n, src, dst, status);
+  const bool with_rows = (int64_t)n * a.width <= kForkRowsInPlan;
+  kv_fork_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, parent, child, n, src, dst, with_rows, status);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || with_rows) return e;
   note_launch();
   const dim3 grid((unsigned)n, (unsigned)((a.width + kRowThreads - 1) / kRowThreads));
   kv_fork_rows_kernel<<<grid, kRowThreads, 0, s>>>(p, parent, child, dst, status);
@@ -271,12 +291,18 @@ cudaError_t launch_kv_free(const PoolArgs& a, const int32_t* which, int n, int* 
 
 // --------------------------------------------------------------- compacting
 // L = used pages. The i-th used page at or above L moves to the i-th free page
-// below L (there are as many of one as of the other). Three launches: used
-// pages of each chunk of 4096; ranks, moves and reference counts; the tables.
-constexpr int kChunkPages = 4 * kPlanThreads;
+// below L (there are as many of one as of the other). Launches: the used pages of
+// each chunk of 4096 (up to 8 chunks are counted in the next one instead: 3 us of
+// host time and a launch less, against reading them all); ranks, moves
+// and reference counts; the tables and the moved pages' counts.
+constexpr int kChunkPages = 4 * kPlanThreads, kSmallChunks = 8;
 
 NVFP4_DEVINL uint32_t used_mask(const int32_t* refs, int64_t at, int64_t n) {
   uint32_t m = 0;
+  if (at + 4 <= n && (reinterpret_cast<uintptr_t>(refs) & 15u) == 0) {  // at is a multiple of 4
+    const int4 r = *reinterpret_cast<const int4*>(refs + at);
+    return (uint32_t)((r.x > 0) | (r.y > 0) << 1 | (r.z > 0) << 2 | (r.w > 0) << 3);
+  }
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (at + e < n && refs[at + e] > 0) m |= 1u << e;
@@ -291,13 +317,28 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_count_kernel(const in
   if (threadIdx.x == 0) counts[blockIdx.x] = sum;
 }
 
-// Used pages in [0, p0 + 4*t) by chunk counts and a scan of one chunk.
 __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const int32_t* refs, int64_t n,
-                                                                       const int32_t* __restrict__ counts, int chunks,
+                                                                       const int32_t* counted, int chunks,
                                                                        int32_t* refs_out, int32_t* src, int32_t* dst,
                                                                        int64_t cap, int32_t* rank_of, int32_t* live) {
   __shared__ int sh[kPlanWarps + 1];
+  __shared__ int32_t small[kSmallChunks];
   const int t = threadIdx.x;
+  const int32_t* counts = counted;
+  if (counted == nullptr) {  // at most kSmallChunks, all loads in flight
+    uint32_t used[kSmallChunks];
+#pragma unroll
+    for (int c = 0; c < kSmallChunks; ++c) used[c] = used_mask(refs, (int64_t)c * kChunkPages + 4 * t, n);
+    if (t < kSmallChunks) small[t] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < kSmallChunks; ++c) {
+      const int sum = __reduce_add_sync(0xFFFFFFFFu, __popc(used[c]));
+      if ((t & 31) == 0) atomicAdd(&small[c], sum);
+    }
+    __syncthreads();
+    counts = small;
+  }
   int total = 0, before = 0;  // used pages in all, and in the chunks before this one
   for (int c0 = 0; c0 < chunks; c0 += kPlanThreads) {
     const int c = c0 + t;
@@ -341,6 +382,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const int
       rank_of[p] = rank - below;
     } else {
       refs_out[p] = 0;
+      rank_of[p] = -1;
     }
     rank += u;
   }
@@ -349,42 +391,37 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const int
   if (blockIdx.x == 0 && t == 0) *live = total;
 }
 
-// blockIdx.y = 0..slots-1: a row of the table; blockIdx.y = slots: the moved
-// pages' reference counts.
+// The first ref_blocks CTAs: the moved pages' reference counts; the others: 256
+// entries of a row of the table each. In place or not: the rows read no counts.
 __global__ void __launch_bounds__(kRowThreads) kv_compact_apply_kernel(PoolIndex p, const int32_t* __restrict__ src,
                                                                        const int32_t* __restrict__ dst, int64_t cap,
                                                                        const int32_t* __restrict__ rank_of,
                                                                        const int32_t* __restrict__ live,
                                                                        int32_t* refs_out, int32_t* table_out,
-                                                                       int* status) {
-  const int64_t step = (int64_t)gridDim.x * kRowThreads;
-  const int64_t j0 = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  const int64_t L = *live;
-  for (int64_t row = blockIdx.y; row < p.slots; row += gridDim.y) {
-    const int64_t held = (slot_len(p, (int32_t)row, status) + (int64_t)p.page - 1) / p.page;
-    for (int64_t j = j0; j < p.width; j += step) {
-      int64_t page = p.table[row * p.width + j];
-      if (j < held) {
-        if (page < 0 || page >= p.num_pages || (page >= L && p.refs[page] <= 0)) {
-          record_status(status, NVFP4_ERR_PAGE);  // not a page of this pool, or one that nobody holds
-        } else if (page >= L) {
-          page = dst[rank_of[page]];
-        }
-      }
-      table_out[row * p.width + j] = (int32_t)page;
+                                                                       int ref_blocks, int* status) {
+  if ((int)blockIdx.x < ref_blocks) {
+    for (int64_t r = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; r < cap; r += (int64_t)ref_blocks * kRowThreads) {
+      const int32_t a = src[r];
+      if (a < 0) return;  // the moves come first
+      const int32_t count = p.refs[a];
+      refs_out[dst[r]] = count;
+      refs_out[a] = 0;
     }
+    return;
   }
-}
-
-__global__ void __launch_bounds__(kRowThreads) kv_compact_refs_kernel(const int32_t* refs, int32_t* refs_out,
-                                                                      const int32_t* __restrict__ src,
-                                                                      const int32_t* __restrict__ dst, int64_t cap) {
-  for (int64_t r = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; r < cap; r += (int64_t)gridDim.x * kRowThreads) {
-    const int32_t a = src[r];
-    if (a < 0) return;  // the moves come first
-    const int32_t count = refs[a];
-    refs_out[dst[r]] = count;
-    refs_out[a] = 0;
+  const int64_t L = *live, pieces = (p.width + kRowThreads - 1) / kRowThreads;
+  for (int64_t x = blockIdx.x - ref_blocks; x < p.slots * pieces; x += gridDim.x - ref_blocks) {
+    const int64_t row = x / pieces, j = (x - row * pieces) * kRowThreads + threadIdx.x;
+    if (j >= p.width) continue;
+    const int64_t held = (slot_len(p, (int32_t)row, status) + (int64_t)p.page - 1) / p.page;
+    int64_t page = p.table[row * p.width + j];
+    if (j < held) {
+      if (page < 0 || page >= p.num_pages || (page >= L && rank_of[page] < 0))
+        record_status(status, NVFP4_ERR_PAGE);  // not a page of this pool, or one that nobody holds
+      else if (page >= L)
+        page = dst[rank_of[page]];
+    }
+    table_out[row * p.width + j] = (int32_t)page;
   }
 }
 
@@ -400,27 +437,25 @@ cudaError_t launch_kv_compact(const PoolArgs& a, int32_t* refs_out, int32_t* tab
   int32_t* rank_of = static_cast<int32_t*>(workspace);
   int32_t* counts = rank_of + n;
   const PoolIndex p{a.refs, a.table, a.seq_len, n, a.slots, a.width, a.page};
-  note_launch();
-  kv_compact_count_kernel<<<chunks, kPlanThreads, 0, s>>>(a.refs, n, counts);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  note_launch();
-  kv_compact_plan_kernel<<<chunks, kPlanThreads, 0, s>>>(a.refs, n, counts, chunks, refs_out, src, dst, cap, rank_of,
-                                                        live);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (a.slots > 0 && a.width > 0) {
+  cudaError_t e;
+  if (chunks > kSmallChunks) {
     note_launch();
-    const unsigned gx = (unsigned)((a.width + kRowThreads - 1) / kRowThreads);
-    const dim3 grid(gx < 64 ? gx : 64, (unsigned)(a.slots < 65535 ? a.slots : 65535));
-    kv_compact_apply_kernel<<<grid, kRowThreads, 0, s>>>(p, src, dst, cap, rank_of, live, refs_out, table_out, status);
+    kv_compact_count_kernel<<<chunks, kPlanThreads, 0, s>>>(a.refs, n, counts);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  const int64_t blocks = (cap + kRowThreads - 1) / kRowThreads;
   note_launch();
-  kv_compact_refs_kernel<<<(int)(blocks < num_sms ? blocks : num_sms), kRowThreads, 0, s>>>(a.refs, refs_out, src, dst,
-                                                                                            cap);
+  kv_compact_plan_kernel<<<chunks, kPlanThreads, 0, s>>>(a.refs, n, chunks > kSmallChunks ? counts : nullptr, chunks,
+                                                        refs_out, src, dst, cap, rank_of, live);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  note_launch();
+  const int64_t refs = (cap + kRowThreads - 1) / kRowThreads, most = 16 * (int64_t)num_sms;
+  const int64_t rows = a.slots * ((a.width + (int64_t)kRowThreads - 1) / kRowThreads);
+  const int ref_blocks = (int)(refs < num_sms ? refs : num_sms);
+  const int row_blocks = (int)(rows < 1 ? 1 : rows < most ? rows : most);
+  kv_compact_apply_kernel<<<ref_blocks + row_blocks, kRowThreads, 0, s>>>(p, src, dst, cap, rank_of, live, refs_out,
+                                                                         table_out, ref_blocks, status);
   return cudaGetLastError();
 }
 
