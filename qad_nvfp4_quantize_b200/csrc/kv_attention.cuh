@@ -221,16 +221,14 @@ struct PartScratch {
 //   runs of kLong / 4 or kLong granules: short works are not cut;
 //   the longest run of which every CTA gets one, if there are few works: no CTA
 //   has the end of one work and the start of another.
-// With kLong = kFine the first is taken. A thread counts a sequence, a warp one
-// of many tiles.
+// A thread counts a sequence, a warp one of many tiles.
 template <int kRows, int kFine, int kLong, int kHead, int kThreads>
-NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& part) {
+NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& part, float join_cost) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kMid = kLong == kFine ? kFine : kLong / 4;
-  constexpr int kKinds = kLong == kFine ? 1 : 3;
+  constexpr int kMid = kLong / 4, kKinds = 3;
   constexpr int kUnit[3] = {kFine, kMid, kLong};
   constexpr int kHeads[3] = {kHead, 0, 0};
-  constexpr float kPieceCost = kHead, kCutCost = 1.5f * kHead;  // and one for each piece that is joined
+  constexpr float kPieceCost = kHead, kCutCost = 1.5f * kHead;  // in units of kFine; join_cost for each piece joined
   constexpr int kSums = kKinds + 1;  // the units of each kind, and the works
   struct Sums {
     int64_t of[kSums];
@@ -327,15 +325,17 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
     };
     int kind = 0, unit = kFine, head_units = kHead;
     int64_t total = all.of[0];
-    if (kKinds > 1) {
+    {
       const int64_t works = all.of[kKinds];
-      const float granules = fmaxf((float)(all.of[0] - works * kHead), 1.0f);
-      float best = (float)parts(all.of[0]) + kPieceCost + kCutCost;
+      const float granules = fmaxf((float)(all.of[0] - works * kHead), 1.0f);  // in units of kFine
+      const float each = granules / (float)works, share = (float)parts(all.of[0]);
+      float best = share + kPieceCost + kCutCost + join_cost * each / share;
 #pragma unroll
       for (int k = 1; k < kKinds; ++k) {
         const bool cut = all.of[k] > works;
-        const float takes = (float)parts(all.of[k]) * (1.125f * granules / (float)all.of[k] + kPieceCost +
-                                                       (cut ? kCutCost + (float)all.of[k] / (float)works : 0.0f));
+        const float takes =
+            (float)parts(all.of[k]) * (1.125f * granules / (float)all.of[k] + kPieceCost +
+                                       (cut ? kCutCost + join_cost * (float)all.of[k] / (float)works : 0.0f));
         if (takes < best) {
           best = takes;
           kind = k;
@@ -343,14 +343,16 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       }
       if (few && 2 * works <= gridDim.x) {  // ceil(n / unit) over the works is at most granules / unit + works
         const int run = (int)ceilf(granules / (float)((int)gridDim.x - (int)works)) + 1;
-        const float takes = (float)run + kPieceCost + kCutCost + granules / (float)run / (float)works;
-        if (takes < best) kind = 3, unit = run;
+        if ((float)run + kPieceCost + kCutCost + join_cost * each / (float)run < best) {
+          kind = 3;
+          unit = run * kFine;
+        }
       }
       if (kind) {
         if (kind < 3) unit = kind == 1 ? kMid : kLong;
         head_units = 0;
         if (kind < 3) {
-          total = kind == 1 ? all.of[1 % kKinds] : all.of[2 % kKinds];
+          total = kind == 1 ? all.of[1] : all.of[2];
         } else {
           int64_t u = 0;
           for (int t = 0; t < tiles_of<kRows>(a, mine); ++t)
@@ -377,7 +379,7 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       base += __shfl_sync(0xFFFFFFFFu, at ? incl - v : incl, src);
       return at ? src : -1;
     };
-    auto of_kind = [&](const Sums& u) { return kind == 1 ? u.of[1 % kKinds] : kind == 2 ? u.of[2 % kKinds] : u.of[0]; };
+    auto of_kind = [&](const Sums& u) { return kind == 1 ? u.of[1] : kind == 2 ? u.of[2] : u.of[0]; };
     int b = -1, tile = -1;
     KvSeq s{0, 0, 0};
     if (u0 < total) {

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     sh.abort = 0;
     fence_barrier_init();
   }
-  find_part<kPreRows, kUnitGranules, kUnitGranules, 0, kPreThreads>(a, sh.scratch, sh.part);
+  find_part<kPreRows, kUnitGranules, 16 * kUnitGranules, 2, kPreThreads>(a, sh.scratch, sh.part, 0.5f);
   if (sh.part.u0 >= sh.part.u1) return;
   const int64_t u0 = sh.part.u0;
   WorkCursor<kPreRows>& w = sh.cursor[warp];
@@ -278,9 +278,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   auto place = [](uint32_t x) { return x % Sh::kTiles; };
   auto turn_of = [](uint32_t x) { return (x / Sh::kTiles) & 1; };
   // units of the work that are this CTA's: its part begins at u0 and at the first unit of every later work
-  // (the reductions make the values warp-uniform to the compiler as well)
-  auto from_unit = [&]() { return uniform((int)(w.w0 < u0 ? u0 - w.w0 : 0)); };
-  auto to_unit = [&]() { return uniform((int)(sh.part.u1 - w.w0 < w.n ? sh.part.u1 - w.w0 : (int64_t)w.n)); };
+  auto from_unit = [&]() { return (int)(w.w0 < u0 ? u0 - w.w0 : 0); };
+  auto to_unit = [&]() { return (int)(sh.part.u1 - w.w0 < w.n ? sh.part.u1 - w.w0 : (int64_t)w.n); };
+  // and their tiles of 128 tokens (the reductions make the values warp-uniform to the compiler as well). A part without
+  // granules (a work that sees nothing, or a cut in front of the first one) takes the tile behind the work's last,
+  // whose tokens are all masked.
+  auto tiles_of_part = [&](int& j0, int& j1) {
+    int g0, g1;
+    w.granules(from_unit(), to_unit(), g0, g1);
+    const int behind = (w.span.n + kUnitGranules - 1) / kUnitGranules;
+    j0 = uniform(g1 > g0 ? g0 / kUnitGranules : behind);
+    j1 = uniform(g1 > g0 ? (g1 + kUnitGranules - 1) / kUnitGranules : behind + 1);
+  };
   auto next_work = [&]() {  // the warp's cursor moves on; false at the end of the part
     __syncwarp();
     int more = 0;
@@ -303,7 +312,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     };
     bool ok = true;
     while (ok) {
-      const int j0 = from_unit(), j1 = to_unit();
+      int j0, j1;
+      tiles_of_part(j0, j1);
       const int32_t nrows = w.seq.rows * a.group;
       const int32_t r0 = w.tile * kPreRows + i * 128, r = r0 + row;
       if (r0 < nrows) {
@@ -442,7 +452,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         // ---- epilogue: O of the last step is complete
         if (!(ok = wait(&sh.pv_done[i][(steps - 1) & 1], ((steps - 1) >> 1) & 1))) break;
         tc_fence_after();
-        const bool whole_work = j0 == 0 && j1 == w.n;
+        const bool whole_work = from_unit() == 0 && to_unit() == w.n;
         const int64_t at = tok * a.ix.hkv * a.group + hq;
         if (m == kStartMax) m = -INFINITY;
         auto write_row = [&](int c, const float* o, float f) {  // 32 dimensions from 32*c
@@ -468,7 +478,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           // part of a work: m, l, then O in pieces of 4 columns x 128 rows
           constexpr int kPart = 128 * (D + 2);
           auto part_of = [&](int64_t cta, bool head_part) { return a.partial + ((2 * cta + head_part) * 2 + i) * kPart; };
-          float* mine_p = part_of(blockIdx.x, j0 == 0);
+          float* mine_p = part_of(blockIdx.x, from_unit() == 0);
           mine_p[row] = m;
           mine_p[128 + row] = l;
 #pragma unroll 1
@@ -527,7 +537,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     uint32_t it = 0;  // K/V tiles done
     bool ok = true;
     while (ok) {
-      for (int x = to_unit() - from_unit(); x > 0; --x, ++it) {
+      int j0, j1;
+      tiles_of_part(j0, j1);
+      for (int x = j1 - j0; x > 0; --x, ++it) {
         const uint32_t st = it % kStages;
         if (!(ok = wait(&sh.codes_full[st], (it / kStages) & 1))) break;
         const uint32_t there = uniform((int)sh.there[st]);
@@ -586,7 +598,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     uint32_t it = 0;
     bool ok = true;
     while (ok) {
-      const int j0 = from_unit(), n = to_unit() - j0;
+      int j0, j1;
+      tiles_of_part(j0, j1);
+      const int n = j1 - j0;
       const int32_t* table = a.ix.table + (int64_t)w.b * a.ix.width;
       const int32_t gend = w.span.g0 + w.span.n;
       const int64_t page_bytes = ((int64_t)a.ix.hkv << a.ix.gshift) * kGB;
@@ -642,7 +656,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         return true;
       };
       while (ok) {
-        const int j0 = from_unit(), j1 = to_unit();
+        int j0, j1;
+        tiles_of_part(j0, j1);
         const int n = j1 - j0;
         if (w.tile * kPreRows + i * 128 < w.seq.rows * a.group) {
           if (!(ok = wait(&sh.q_full[i], works & 1))) break;
