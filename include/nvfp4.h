@@ -419,14 +419,14 @@ nvfp4_status nvfp4_kv_copy_pages(uint8_t* pages, int64_t num_pages, int64_t page
                                  nvfp4_stream_t stream);
 
 /*
- * nvfp4_kv_fork -- slot child[i] becomes a copy of slot parent[i], i < n: full
- *   pages are shared (refs + 1); a part page gets a page of its own, the lowest
- *   free ones in the order of i. src[i], dst[i]: the part page and the child's
- *   page (copy them), -1 where there is none, -2 where the entry was refused:
- *   a slot out of range, parent == child, a child that holds tokens or that an
- *   earlier entry names (NVFP4_ERR_PAGE). With too few free pages nothing
- *   changes, every src and dst is -2 and the device status NVFP4_ERR_NO_PAGES.
- *   A child's tokens at or behind its parent's are not set in block_table.
+ * nvfp4_kv_fork -- slot child[i] becomes a copy of slot parent[i] as it was
+ *   before the call, i < n: full pages are shared (refs + 1); a part page gets a
+ *   page of its own, the lowest free ones in the order of i. src[i], dst[i]: the
+ *   part page and the child's page (copy them), -1 where there is none, -2 where
+ *   the entry was refused: a slot out of range, parent == child, a child that
+ *   holds tokens or that an earlier entry names (NVFP4_ERR_PAGE). With too few
+ *   free pages nothing changes, every src and dst is -2 and the device status
+ *   NVFP4_ERR_NO_PAGES. Entries of a child's row behind its last page stay.
  */
 nvfp4_status nvfp4_kv_fork(int32_t* refs, int64_t num_pages, int32_t* block_table, int slots,
                            int table_width, int32_t* seq_len, int page_size, const int32_t* parent,

@@ -87,6 +87,17 @@ std::atomic<uint64_t> g_launches{0};
 
 void nvfp4::note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
+cudaError_t nvfp4::allow_dynamic_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);  // the device gate admits kMaxDevices = 64 devices
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 int nvfp4::current_device_context(int* num_sms, int** status) {
   DeviceInfo* d;
   const nvfp4_status st = current_device(&d);
@@ -99,7 +110,7 @@ int nvfp4::current_device_context(int* num_sms, int** status) {
 
 extern "C" {
 
-int nvfp4_version(void) { return 100; }
+int nvfp4_version(void) { return 200; }
 
 nvfp4_status nvfp4_check_device(void) {
   DeviceInfo* d;

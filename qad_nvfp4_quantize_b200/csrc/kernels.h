@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace nvfp4 {
 
 constexpr int kMaxPartials = 1024;  // amax pass-1 partial slots in a workspace
@@ -89,6 +91,10 @@ struct MoeArgs {
 };
 int64_t moe_rows_capacity(int64_t T, int topk, int E);
 cudaError_t launch_moe(const MoeArgs& a, int* status, int num_sms, cudaStream_t s);
+
+// Dynamic shared memory above 48 KB for a kernel, set once for each device that
+// launches it (`done`: a word of the kernel's own, a bit for each device).
+cudaError_t allow_dynamic_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 // Paged NVFP4 KV cache (kv_append.cu, kv_pages.cu, kv_attention.cu).
 struct KvIndex;

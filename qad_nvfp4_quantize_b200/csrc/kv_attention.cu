@@ -540,9 +540,9 @@ size_t kv_attention_workspace_bytes() {
 template <int D, int NT>
 cudaError_t launch_rows(AttnArgs a, int num_sms, cudaStream_t s) {
   using Sh = AttnShared<D, NT>;
-  static const cudaError_t attr = cudaFuncSetAttribute(kv_attention_kernel<D, NT>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Sh));
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(&kv_attention_kernel<D, NT>), sizeof(Sh), done);
+  if (e != cudaSuccess) return e;
   const int64_t want = (NT == 1 ? 2 : 1) * (int64_t)num_sms;
   const int grid = (int)(want < kMaxAttnCtas ? want : kMaxAttnCtas);
   note_launch();
@@ -557,7 +557,7 @@ cudaError_t launch_kv_attention(AttnArgs a, int D, int64_t max_q, void* workspac
   // Rows of a KV head: up to 8 a tile of 8, up to 32 tiles of 16, above tiles of 256 on tcgen05. Measured with 32
   // sequences of 8,192 tokens, 4 KV heads of 128: 8 rows 53 us in a tile of 8 and 68 in one of 16; 16 rows 84, 70 and
   // 122 us on tcgen05; 32 rows 139, 111 and 123; with 64 sequences of 512 tokens and 64 rows 131, 133 and 64.
-  if (max_q == 0 || max_q * a.group > 32) return launch_kv_prefill(a, D, num_sms, s);
+  if (max_q == 0 || max_q > 32 || max_q * a.group > 32) return launch_kv_prefill(a, D, num_sms, s);
   const bool one = max_q * a.group <= 8;
   if (D == 128) return one ? launch_rows<128, 1>(a, num_sms, s) : launch_rows<128, 2>(a, num_sms, s);
   return one ? launch_rows<64, 1>(a, num_sms, s) : launch_rows<64, 2>(a, num_sms, s);

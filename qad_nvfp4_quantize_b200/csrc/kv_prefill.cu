@@ -718,9 +718,9 @@ template <int D>
 cudaError_t launch_tiles(const AttnArgs& a, int num_sms, cudaStream_t s) {
   constexpr int bytes = (int)sizeof(PreShared<D>) + 1024;
   static_assert(bytes <= 232448, "shared memory budget");
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(&kv_prefill_kernel<D>), bytes, done);
+  if (e != cudaSuccess) return e;
   note_launch();
   kv_prefill_kernel<D><<<num_sms < kMaxPreCtas ? num_sms : kMaxPreCtas, kPreThreads, bytes, s>>>(a);
   return cudaGetLastError();
