@@ -183,7 +183,8 @@ def _reset_workspaces(device_index: int) -> None:
     """Zero-fill every cached workspace of one device (after a timed-out wait).
     Each is cleared on the stream that uses it, after the work queued there."""
     with _ws_lock:
-        items = [entry for cache in (_ws_cache, _attn_ws) for key, entry in cache.items() if key[0] == device_index]
+        items = [entry for key, entry in _ws_cache.items() if key[0] == device_index]
+        items += [(entry[3], entry[2]) for key, entry in _attn_ws.items() if key[0] == device_index]
     for stream, ws in items:
         with torch.cuda.stream(stream):
             ws.zero_()
@@ -429,12 +430,11 @@ _INT32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
 
 def _ints(t: torch.Tensor, name: str, index: int, *shape) -> int:
     """Checks a contiguous int32 tensor on GPU `index` (None in shape: any size); returns its address."""
+    if t.dtype is not _INT32 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous torch.int32 tensor on cuda:{index}")
     got = t.shape
-    if t.dtype is not _INT32 or t.get_device() != index or not t.is_contiguous() or len(got) != len(shape):
-        raise ValueError(f"{name} must be a contiguous torch.int32 tensor of {len(shape)} dimension(s) on cuda:{index}")
-    for want, have in zip(shape, got):
-        if want is not None and want != have:
-            raise ValueError(f"{name} must have shape {list(shape)}, got {list(got)}")
+    if got != shape and (len(got) != len(shape) or any(x is not None and x != y for x, y in zip(shape, got))):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(got)}")
     return t.data_ptr()
 
 
@@ -470,7 +470,7 @@ def _kv_cache_of(cache: KVCache):
 def _call(name: str, index: int, *args) -> None:
     """A C entry point on GPU `index`, on torch's current stream there."""
     fn = getattr(_lib or lib(), name)
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
@@ -487,21 +487,22 @@ _ATTN_COUNTERS = 2048
 _attn_ws: dict = {}
 
 
-def _attention_workspace(index: int) -> torch.Tensor:
-    if index != torch.cuda.current_device():
+def _attention_workspace(index: int):
+    """(address, bytes) of the workspace of the current stream of GPU `index`, and its tensor."""
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _attention_workspace(index)
+    capturing = torch._C._cuda_isCurrentStreamCapturing()
     key = (index, torch._C._cuda_getCurrentRawStream(index))
-    capturing = torch.cuda.is_current_stream_capturing()
     entry = None if capturing else _attn_ws.get(key)
     if entry is None:
         ws = torch.empty(int(lib().nvfp4_paged_attention_workspace_bytes()), dtype=torch.uint8, device=f"cuda:{index}")
         ws[:_ATTN_COUNTERS].zero_()
-        if capturing:
-            return ws
-        with _ws_lock:
-            entry = _attn_ws.setdefault(key, (torch.cuda.current_stream(index), ws))
-    return entry[1]
+        entry = (ws.data_ptr(), ws.numel(), ws, torch.cuda.current_stream(index))
+        if not capturing:
+            with _ws_lock:
+                entry = _attn_ws.setdefault(key, entry)
+    return entry
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, cu_q: torch.Tensor,
@@ -514,10 +515,10 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
     stride = _rows(k, "k", index, heads, cache.head_dim)
     if _rows(v, "v", index, heads, cache.head_dim) != stride or v.shape != k.shape:
         raise ValueError("k and v must have the same shape and strides")
-    batch = kv_len.shape[0]
+    batch, width = kv_len.shape[0], block_table.shape[-1]
     _call("nvfp4_kv_append", index, k.data_ptr(), v.data_ptr(), stride, k.shape[0], heads, cache.head_dim,
           _ints(cu_q, "cu_q", index, batch + 1), _ints(kv_len, "kv_len", index, batch), batch,
-          _ints(block_table, "block_table", index, batch, None), block_table.shape[1], cache.pages.data_ptr(), num_pages,
+          _ints(block_table, "block_table", index, batch, width), width, cache.pages.data_ptr(), num_pages,
           cache.page_size, cache.k_g.data_ptr(), cache.v_g.data_ptr(), _MODES[mode])
 
 
@@ -536,8 +537,9 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     stride = _rows(q, "q", index, None, dim)
     total, hq, _ = q.shape
     batch = kv_len.shape[0]
+    width = block_table.shape[-1]
     seqs = (_ints(cu_q, "cu_q", index, batch + 1), _ints(kv_len, "kv_len", index, batch), batch,
-            _ints(block_table, "block_table", index, batch, None), block_table.shape[1])
+            _ints(block_table, "block_table", index, batch, width), width)
     if out is None:
         out = torch.empty((total, hq, dim), dtype=_BF16, device=q.device)
     elif out.shape != q.shape or out.dtype is not _BF16 or out.get_device() != index or not out.is_contiguous():
@@ -550,11 +552,11 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
         lse_out = torch.empty((total, hq), dtype=_F32, device=q.device)
     if max_q is None:
         max_q = 1 if total <= batch else 0
-    ws = _attention_workspace(index)
+    ws, ws_bytes, _keep, _ = _attention_workspace(index)
     _call("nvfp4_paged_attention", index, q.data_ptr(), stride, total, hq, heads, dim, *seqs, cache.pages.data_ptr(),
           num_pages, cache.page_size, cache.k_g.data_ptr(), cache.v_g.data_ptr(), dim ** -0.5 if scale is None else scale,
-          int(causal), window, max_q, out.data_ptr(), None if lse_out is None else lse_out.data_ptr(), ws.data_ptr(),
-          ws.numel())
+          int(causal), window, max_q, out.data_ptr(), None if lse_out is None else lse_out.data_ptr(), ws,
+          ws_bytes)
     return out, lse_out
 
 
@@ -572,10 +574,9 @@ def _pool(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor, 
     index = refs.get_device()
     if index < 0:
         raise ValueError("refs must be a CUDA tensor")
-    slots = seq_len.shape[0]
-    return index, (_ints(refs, "refs", index, None), refs.shape[0],
-                   _ints(block_table, "block_table", index, slots, None), slots, block_table.shape[1],
-                   _ints(seq_len, "seq_len", index, slots), page_size)
+    pages, slots, width = refs.shape[0], seq_len.shape[0], block_table.shape[-1]
+    return index, (_ints(refs, "refs", index, pages), pages, _ints(block_table, "block_table", index, slots, width), slots,
+                   width, _ints(seq_len, "seq_len", index, slots), page_size)
 
 
 def kv_fork(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor, parent: torch.Tensor,

