@@ -37,9 +37,15 @@ constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kLongUnit = 384, kHeadUnits = 60;  // granules
 constexpr int kMaxAttnCtas = 320;
 
+// Two CTAs for each SM where 128 registers a thread hold the output and the
+// queries: 16 rows of 128 dimensions need 230 (with 128 and spills, 16 rows over
+// 2,048 cached tokens took 33 us instead of 25).
+template <int D, int NT>
+constexpr int kCtasPerSm = NT == 1 || D == 64 ? 2 : 1;
+
 template <int D, int NT>
 struct AttnShared {
-  static constexpr int kStages = 3;  // pairs of granules in flight for each warp
+  static constexpr int kStages = 2;  // pairs of granules that a warp works on or has in flight
   static constexpr int kRows = 8 * NT;
   static constexpr int kPad = D + 8;  // row pitch of the joining buffer
   union {
@@ -80,7 +86,7 @@ __host__ __device__ constexpr int token_of(int i) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attention_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_kernel(const AttnArgs a) {
   using Sh = AttnShared<D, NT>;
   extern __shared__ __align__(128) uint8_t attn_smem[];
   Sh& sh = *reinterpret_cast<Sh*>(attn_smem);
@@ -543,7 +549,7 @@ cudaError_t launch_rows(AttnArgs a, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(&kv_attention_kernel<D, NT>), sizeof(Sh), done);
   if (e != cudaSuccess) return e;
-  const int64_t want = (NT == 1 ? 2 : 1) * (int64_t)num_sms;
+  const int64_t want = kCtasPerSm<D, NT> * (int64_t)num_sms;
   const int grid = (int)(want < kMaxAttnCtas ? want : kMaxAttnCtas);
   note_launch();
   kv_attention_kernel<D, NT><<<grid, kAttnThreads, sizeof(Sh), s>>>(a);
