@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
   if (tid == 0) sh.abort = 0;
   fence_barrier_init();
 
+  prefetch_inputs(a, D);
   find_part<kRows, 1, kLongUnit, kHeadUnits, kAttnThreads>(a, sh.scratch, sh.part, 1.0f);
   const int64_t u0 = sh.part.u0, u1 = sh.part.u1, per = sh.part.per;
   if (u0 >= u1) return;
@@ -118,6 +119,26 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
     const int tile = w.tile, head = w.head, b = w.b;
     int j0, j1;  // granules
     w.granules(unit0, unit1, j0, j1);
+
+    // ---- the queries' rows are on their way first: row r = tile*kRows + 8*nt + g of the head's rows
+    const int32_t nrows = seq.rows * a.group;
+    uint32_t raw[NT][D / 8];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int32_t r = tile * kRows + 8 * nt + g;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) raw[nt][i] = 0;
+      if (r < nrows) {
+        const int32_t tok = a.by_group.divide(r), hq = head * a.group + r - tok * a.group;
+        const uint4* q4 =
+            reinterpret_cast<const uint4*>(a.q + (seq.row0 + tok) * a.q_stride + (int64_t)hq * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 v = ld_stream(q4 + i);
+          raw[nt][4 * i] = v.x; raw[nt][4 * i + 1] = v.y; raw[nt][4 * i + 2] = v.z; raw[nt][4 * i + 3] = v.w;
+        }
+      }
+    }
 
     // ---- this warp's pairs of granules j0 + 2*(warp + 8*i) and the next one; the first ones are fetched while the
     // queries are prepared
@@ -158,38 +179,23 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       if ((ahead & 15) == 0) there = there_next;
     }
 
-    // ---- queries: B fragments of Q^T, row r = tile*kRows + 8*nt + g of the head's rows
+    // ---- queries: B fragments of Q^T
     uint32_t qf[NT][2 * kSteps];
     float factor[NT][2];        // score units of columns 2t, 2t+1
     int32_t lo[NT][2], hi[NT][2];
     int32_t all_lo = 0, all_hi = 0x7FFFFFFF;  // tokens that every row of the tile sees
-    const int32_t nrows = seq.rows * a.group;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int32_t r = tile * kRows + 8 * nt + g;
-      uint32_t raw[D / 8];
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) raw[i] = 0;
-      if (r < nrows) {
-        const int32_t tok = r / a.group, hq = head * a.group + r - tok * a.group;
-        const uint4* q4 =
-            reinterpret_cast<const uint4*>(a.q + (seq.row0 + tok) * a.q_stride + (int64_t)hq * D + t * (D / 4));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 v = ld_stream(q4 + i);
-          raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
-        }
-      }
       uint32_t mx = 0;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) mx = max(mx, mag_max_halves(raw[i]));
+      for (int i = 0; i < D / 8; ++i) mx = max(mx, mag_max_halves(raw[nt][i]));
       mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
       const int ex = query_exponent(__uint_as_float(mx << 16));
 #pragma unroll
       for (int e = 0; e < 4 * kWords; ++e)
-        qf[nt][e] = half2_bits(scale_exp2(__uint_as_float(raw[e] << 16), ex),
-                               scale_exp2(__uint_as_float(raw[e] & 0xFFFF0000u), ex));
+        qf[nt][e] = half2_bits(scale_exp2(__uint_as_float(raw[nt][e] << 16), ex),
+                               scale_exp2(__uint_as_float(raw[nt][e] & 0xFFFF0000u), ex));
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int32_t rc = tile * kRows + 8 * nt + 2 * t + c;
@@ -197,7 +203,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
         // not zero: a masked score is -Inf before it is multiplied
         factor[nt][c] = fmaxf(scale_exp2(a.scale * kg * kLog2e, kValueExp - ec), 1.17549435e-38f);
         Visible v{0, 0};
-        if (rc < nrows) v = visible(seq.len - seq.rows + rc / a.group, seq.len, a.causal, a.window);
+        if (rc < nrows) v = visible(seq.len - seq.rows + a.by_group.divide(rc), seq.len, a.causal, a.window);
         lo[nt][c] = v.lo;
         hi[nt][c] = v.hi;
         if (rc < nrows) {
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
         const int e = e0 + tid, row = e / (D / 4), d = (e % (D / 4)) * 4;
         const int32_t r = tile * kRows + row;
         if (r >= nrows || (kRows * (D / 4) < kAttnThreads && e >= kRows * (D / 4))) continue;
-        const int32_t tok = r / a.group, hq = head * a.group + r - tok * a.group;
+        const int32_t tok = a.by_group.divide(r), hq = head * a.group + r - tok * a.group;
         const int64_t at = (seq.row0 + tok) * a.ix.hkv * a.group + hq;
         const float lt = sh.l[row];
         const float f = lt == 0.0f ? 0.0f : kValueScale * vg / lt;  // no visible token: zeros
@@ -551,6 +557,7 @@ cudaError_t launch_rows(AttnArgs a, int num_sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t want = kCtasPerSm<D, NT> * (int64_t)num_sms;
   const int grid = (int)(want < kMaxAttnCtas ? want : kMaxAttnCtas);
+  a.by_grid = Divisor(grid);
   note_launch();
   kv_attention_kernel<D, NT><<<grid, kAttnThreads, sizeof(Sh), s>>>(a);
   return cudaGetLastError();
@@ -558,6 +565,7 @@ cudaError_t launch_rows(AttnArgs a, int num_sms, cudaStream_t s) {
 
 cudaError_t launch_kv_attention(AttnArgs a, int D, int64_t max_q, void* workspace, int num_sms, cudaStream_t s) {
   if (a.ix.total == 0 || a.ix.batch == 0) return cudaSuccess;
+  a.by_group = Divisor(a.group);
   a.counters = static_cast<int32_t*>(workspace);
   a.partial = reinterpret_cast<float*>(a.counters + kCounters);
   // Rows of a KV head: up to 8 a tile of 8, up to 32 tiles of 16, above tiles of 256 on tcgen05. Measured with 32

@@ -79,6 +79,22 @@ NVFP4_DEVINL Visible visible(int64_t pos, int32_t len, int causal, int64_t windo
   return Visible{(int32_t)lo, (int32_t)hi};
 }
 
+// Division of 0 <= n < 2^31 by a divisor known to the host: with l = ceil(log2 d)
+// and m = floor(2^(31+l) / d) + 1, m * d exceeds 2^(31+l) by at most 2^l, which
+// no such n notices.
+struct Divisor {
+  uint32_t d, m;
+  int shift;
+  Divisor() = default;
+  explicit Divisor(uint32_t of) : d(of) {
+    int l = 0;
+    while ((uint64_t(1) << l) < of) ++l;
+    shift = 31 + l;
+    m = (uint32_t)((uint64_t(1) << shift) / of + 1);
+  }
+  NVFP4_DEVINL int32_t divide(int32_t n) const { return (int32_t)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+
 struct AttnArgs {
   const uint16_t* q;   // BF16 [total][hq][D], rows q_stride apart
   int64_t q_stride;
@@ -87,6 +103,7 @@ struct AttnArgs {
   const float *k_g, *v_g;
   float scale;         // softmax scale
   int group;           // query heads per KV head
+  Divisor by_group, by_grid;
   int causal;
   int64_t window;      // 0: no window
   uint16_t* out;       // BF16 [total][hq][D]
@@ -133,6 +150,20 @@ NVFP4_DEVINL bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abo
   }
 }
 
+// The queries and the page table, asked for while the lengths are on their way:
+// what find_part's caller reads next then waits in L2. A line each thread; what
+// lies behind the grid's first line each is left out.
+NVFP4_DEVINL void prefetch_inputs(const AttnArgs& a, int head_dim) {
+  auto ask = [](const void* p, int64_t bytes, int64_t at) {
+    if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + at));
+  };
+  const int64_t at = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 128;
+  ask(a.q, ((a.ix.total - 1) * a.q_stride + (int64_t)a.ix.hkv * a.group * head_dim) * 2, at);
+  ask(a.ix.table, (int64_t)a.ix.batch * a.ix.width * 4, at);
+  ask(a.k_g, 4, at);
+  ask(a.v_g, 4, at);
+}
+
 // ---------------------------------------------------------------------------
 // Work list. A work is one KV head of one tile of kRows query rows of one
 // sequence (row r = new token r / group, query head r % group of the KV head);
@@ -150,7 +181,7 @@ template <int kRows>
 NVFP4_DEVINL Span tile_span(const AttnArgs& a, const KvSeq& s, int tile) {
   const int32_t rows = s.rows * a.group;
   const int32_t r1 = rows - tile * kRows < kRows ? rows : (tile + 1) * kRows;
-  const int32_t first = tile * kRows / a.group, last = (r1 - 1) / a.group, pos = s.len - s.rows;
+  const int32_t first = a.by_group.divide(tile * kRows), last = a.by_group.divide(r1 - 1), pos = s.len - s.rows;
   const Visible v0 = visible((int64_t)pos + first, s.len, a.causal, a.window);
   const Visible v1 = visible((int64_t)pos + last, s.len, a.causal, a.window);
   if (v1.hi <= v0.lo) return Span{0, 0};
@@ -320,7 +351,7 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
     warp_sum(all);
     // (a 64-bit division takes as long as all the rest of this)
     auto parts = [&](int64_t total) {
-      return total < (int64_t(1) << 31) ? (int64_t)(((uint32_t)total + gridDim.x - 1) / gridDim.x)
+      return total < (int64_t(1) << 30) ? (int64_t)a.by_grid.divide((int32_t)total + (int)gridDim.x - 1)
                                         : (total + gridDim.x - 1) / gridDim.x;
     };
     int kind = 0, unit = kFine, head_units = kHead;
@@ -328,22 +359,22 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
     {
       const int64_t works = all.of[kKinds];
       const float granules = fmaxf((float)(all.of[0] - works * kHead), 1.0f);  // in units of kFine
-      const float each = granules / (float)works, share = (float)parts(all.of[0]);
-      float best = share + kPieceCost + kCutCost + join_cost * each / share;
+      const float each = __fdividef(granules, (float)works), share = (float)parts(all.of[0]);
+      float best = share + kPieceCost + kCutCost + join_cost * __fdividef(each, share);
 #pragma unroll
       for (int k = 1; k < kKinds; ++k) {
         const bool cut = all.of[k] > works;
         const float takes =
-            (float)parts(all.of[k]) * (1.125f * granules / (float)all.of[k] + kPieceCost +
-                                       (cut ? kCutCost + join_cost * (float)all.of[k] / (float)works : 0.0f));
+            (float)parts(all.of[k]) * (__fdividef(1.125f * granules, (float)all.of[k]) + kPieceCost +
+                                       (cut ? kCutCost + join_cost * __fdividef((float)all.of[k], (float)works) : 0.0f));
         if (takes < best) {
           best = takes;
           kind = k;
         }
       }
       if (few && 2 * works <= gridDim.x) {  // ceil(n / unit) over the works is at most granules / unit + works
-        const int run = (int)ceilf(granules / (float)((int)gridDim.x - (int)works)) + 1;
-        if ((float)run + kPieceCost + kCutCost + join_cost * each / (float)run < best) {
+        const int run = (int)ceilf(__fdividef(granules, (float)((int)gridDim.x - (int)works))) + 1;
+        if ((float)run + kPieceCost + kCutCost + join_cost * __fdividef(each, (float)run) < best) {
           kind = 3;
           unit = run * kFine;
         }

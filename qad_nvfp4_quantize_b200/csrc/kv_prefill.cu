@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     sh.abort = 0;
     fence_barrier_init();
   }
+  prefetch_inputs(a, D);
   find_part<kPreRows, kUnitGranules, 16 * kUnitGranules, 2, kPreThreads>(a, sh.scratch, sh.part, 0.5f);
   if (sh.part.u0 >= sh.part.u1) return;
   const int64_t u0 = sh.part.u0;
@@ -319,7 +320,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       if (r0 < nrows) {
         // ---- this thread's query row as FP16, its power of two taken out
         const bool live = r < nrows;
-        const int64_t tok = w.seq.row0 + r / a.group, hq = (int64_t)w.head * a.group + r % a.group;
+        const int32_t t = a.by_group.divide(r);
+        const int64_t tok = w.seq.row0 + t, hq = (int64_t)w.head * a.group + r - t * a.group;
         const uint4* q4 = reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + hq * D);
         uint32_t mx = 0;
         if (live)
@@ -348,9 +350,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         const float factor = fmaxf(scale_exp2(a.scale * kg * kLog2e, kValueExp - ex), 1.17549435e-38f);
         const int64_t pos0 = (int64_t)w.seq.len - w.seq.rows;
         const int32_t r_last = (nrows - r0 < 128 ? nrows : r0 + 128) - 1;
-        const Visible first_row = visible(pos0 + r0 / a.group, w.seq.len, a.causal, a.window);
-        const Visible last_row = visible(pos0 + r_last / a.group, w.seq.len, a.causal, a.window);
-        Visible mine = visible(pos0 + r / a.group, w.seq.len, a.causal, a.window);
+        const Visible first_row = visible(pos0 + a.by_group.divide(r0), w.seq.len, a.causal, a.window);
+        const Visible last_row = visible(pos0 + a.by_group.divide(r_last), w.seq.len, a.causal, a.window);
+        Visible mine = visible(pos0 + t, w.seq.len, a.causal, a.window);
         if (!live) mine = Visible{0, 0x7FFFFFFF};  // never written
         // lanes 0..3: the pages of the next step's granules (0 behind the span), looked at one step later
         const int32_t* table = a.ix.table + (int64_t)w.b * a.ix.width;
@@ -715,14 +717,16 @@ constexpr int kMaxPreCtas = 160;
 size_t kv_prefill_partial_floats() { return (size_t)kMaxPreCtas * 4 * 128 * (128 + 2); }
 
 template <int D>
-cudaError_t launch_tiles(const AttnArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_tiles(AttnArgs a, int num_sms, cudaStream_t s) {
   constexpr int bytes = (int)sizeof(PreShared<D>) + 1024;
   static_assert(bytes <= 232448, "shared memory budget");
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(&kv_prefill_kernel<D>), bytes, done);
   if (e != cudaSuccess) return e;
+  const int grid = num_sms < kMaxPreCtas ? num_sms : kMaxPreCtas;
+  a.by_grid = Divisor(grid);
   note_launch();
-  kv_prefill_kernel<D><<<num_sms < kMaxPreCtas ? num_sms : kMaxPreCtas, kPreThreads, bytes, s>>>(a);
+  kv_prefill_kernel<D><<<grid, kPreThreads, bytes, s>>>(a);
   return cudaGetLastError();
 }
 
