@@ -36,6 +36,8 @@ constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kLongUnit = 384, kHeadUnits = 60;  // granules
 constexpr int kMaxAttnCtas = 320;
+constexpr int kJoin = 16;  // parts joined at a time
+static_assert(kMaxAttnCtas / kJoin >= kJoin && kMaxAttnCtas % kJoin == 0, "space for the parts that are joined");
 
 // Two CTAs for each SM where 128 registers a thread hold the output and the
 // queries: 16 rows of 128 dimensions need 230 (with 128 and spills, 16 rows over
@@ -51,7 +53,7 @@ struct AttnShared {
   union {
     uint8_t ring[kAttnWarps][kStages][2 * granule_bytes(D)];
     float join[kAttnWarps][kRows][kPad];
-    float parts[2][kMaxAttnCtas][kRows];
+    float parts[2][kMaxAttnCtas / kJoin][kRows];
     PartScratch scratch;
   };
   Part<8 * NT> part;
@@ -473,39 +475,44 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       return x;
     };
     constexpr int kPart = kRows * (D + 2);  // O, then m and l of each row
-    if (whole_work) {
-      write_rows(joined);
-    } else {
-      float* part = a.partial + (2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0)) * kPart;
+    auto write_part = [&](float* part, auto&& value) {
       for (int e = tid; e < kRows * (D / 4); e += kAttnThreads) {
         const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-        *reinterpret_cast<float4*>(part + row * D + d) = joined(row, d);
+        *reinterpret_cast<float4*>(part + row * D + d) = value(row, d);
       }
       if (tid < kRows) {
         part[kRows * D + tid] = sh.m[tid];
         part[kRows * D + kRows + tid] = sh.l[tid];
       }
+    };
+    if (whole_work) {
+      write_rows(joined);
+    } else {
+      write_part(a.partial + (2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0)) * kPart, joined);
       __syncthreads();
-      const int64_t c0 = w.w0 / per, c1 = (w.w0 + w.n - 1) / per;  // the CTAs that share the work
-      if (tid == 0) sh.last = arrive_last(a.counters + c0, (int)(c1 - c0));
-      __syncthreads();
-      if (sh.last) {
-        // m and l of all parts, then the factors 2^(m_c - m), then O with eight parts' loads in flight
-        const int np = (int)(c1 - c0) + 1;
-        float *ms = &sh.parts[0][0][0], *ls = &sh.parts[1][0][0];  // [np][kRows]; ms becomes the factors
-        auto part_of = [&](int c) { return a.partial + (2 * (c0 + c) + (c == 0 ? 1 : 0)) * kPart; };
-        for (int x = tid; x < np * kRows; x += kAttnThreads) {
-          const float* p = part_of(x / kRows) + kRows * D + x % kRows;
+      const int c0 = (int)(w.w0 / per), np = (int)((w.w0 + w.n - 1) / per) - c0 + 1;  // the CTAs that share the work
+      for (int round = np > kJoin ? 0 : 1; round < 2; ++round) {
+        const int stride = round == 1 && np > kJoin ? kJoin : 1, first = round == 0 ? ((int)blockIdx.x - c0) / kJoin * kJoin : 0;
+        const int n = round == 0 ? min(kJoin, np - first) : (np + stride - 1) / stride;
+        if (n == 1) continue;  // a run of one part is joined already
+        if (tid == 0) sh.last = arrive_last(a.counters + (round == 0 ? kMaxAttnCtas : 0) + c0 + first, n - 1);
+        __syncthreads();
+        if (!sh.last) break;
+        // m and l of the parts, then the factors 2^(m_c - m), then O with eight parts' loads in flight
+        float *ms = &sh.parts[0][0][0], *ls = &sh.parts[1][0][0];  // [n][kRows]; ms becomes the factors
+        auto part_of = [&](int c) { return a.partial + (2 * (int64_t)(c0 + c) + (c == 0 ? 1 : 0)) * kPart; };
+        for (int x = tid; x < n * kRows; x += kAttnThreads) {
+          const float* p = part_of(first + x / kRows * stride) + kRows * D + x % kRows;
           ms[x] = __ldcg(p);
           ls[x] = __ldcg(p + kRows);
         }
         __syncthreads();
         for (int row = warp; row < kRows; row += kAttnWarps) {
           float mt = -INFINITY, lt = 0.0f;
-          for (int c = lane; c < np; c += 32) mt = fmaxf(mt, ms[c * kRows + row]);
+          for (int c = lane; c < n; c += 32) mt = fmaxf(mt, ms[c * kRows + row]);
 #pragma unroll
           for (int x = 16; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, x));
-          for (int c = lane; c < np; c += 32) {
+          for (int c = lane; c < n; c += 32) {
             const float mc = ms[c * kRows + row];
             const float f = mc == -INFINITY ? 0.0f : ex2(mc - mt);
             ms[c * kRows + row] = f;
@@ -519,20 +526,32 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
           }
         }
         __syncthreads();
-        write_rows([&](int row, int d) {
+        auto sum = [&](int row, int d) {
           float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          const float* p = part_of(0) + row * D + d;  // the later parts lie 2 * kPart apart, the first one kPart behind
-#pragma unroll 16
-          for (int c = 0; c < np; ++c) {
-            const float f = ms[c * kRows + row];
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + (c == 0 ? 0 : (2 * c - 1) * kPart)));
-            x.x += y.x * f;
-            x.y += y.y * f;
-            x.z += y.z * f;
-            x.w += y.w * f;
+          for (int i = 0; i < n; i += 8) {
+            float4 y[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              y[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (i + c < n)
+                y[c] = __ldcg(reinterpret_cast<const float4*>(part_of(first + (i + c) * stride) + row * D + d));
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float f = i + c < n ? ms[(i + c) * kRows + row] : 0.0f;
+              x.x += y[c].x * f;
+              x.y += y[c].y * f;
+              x.z += y[c].z * f;
+              x.w += y[c].w * f;
+            }
           }
           return x;
-        });
+        };
+        if (round == 1)
+          write_rows(sum);
+        else
+          write_part(part_of(first), sum);  // each thread over what it alone has read; m and l after everyone
+        __syncthreads();
       }
     }
     fence_proxy_async_smem();  // the joining buffer's place is filled by bulk copies again
@@ -541,7 +560,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
   }
 }
 
-constexpr int kCounters = 512;
+constexpr int kCounters = 2 * kMaxAttnCtas;  // of works, then of runs of kJoin parts
 constexpr int kPartFloats = 16 * (128 + 2);
 
 size_t kv_attention_workspace_bytes() {
