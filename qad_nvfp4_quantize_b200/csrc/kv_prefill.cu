@@ -3,7 +3,11 @@
 //
 // Bound: the tensor pipe (4*D FLOP per row and token), the 2^x unit (16 a cycle
 // and SM: as long as the two MMAs of a 128 x 128 tile with D = 128) and the
-// issue slots that dequantization and softmax share.
+// issue slots that dequantization and softmax share. Measured, 32 heads over 8 KV
+// heads of 128: 4,096 tokens over 12,288 cached ones (687 GFLOP) in 650 us, 1.06
+// PFLOP/s; 4 chunks of 512 over 16,384 (315 GFLOP) in 343 us. Shared memory is
+// then 76 % busy (49 % the MMAs' operands, 28 % loads and stores), the tensor
+// pipe 49 % and the issue slots 50 %.
 //
 // One CTA per SM walks its part of the work list; a work is 256 query rows (two
 // tiles of 128) of one KV head against its cached tokens, 128 at a time.
