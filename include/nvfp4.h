@@ -368,7 +368,7 @@ nvfp4_status nvfp4_kv_append(const void* k, const void* v, int64_t row_stride, i
                              int64_t num_pages, int page_size, const float* k_g, const float* v_g,
                              nvfp4_mode mode, nvfp4_stream_t stream);
 
-/* Workspace bytes of nvfp4_paged_attention. Zero-fill its first 2048 bytes once
+/* Workspace bytes of nvfp4_paged_attention. Zero-fill its first 4096 bytes once
  * before the first use; every call leaves them ready for the next (zero-fill
  * them again after a call that reported NVFP4_ERR_TIMEOUT). Calls that share a
  * workspace must be ordered on the GPU. Host only. */

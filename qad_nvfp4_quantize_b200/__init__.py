@@ -483,7 +483,7 @@ def _call(name: str, index: int, *args) -> None:
 # One per (device, stream) outside of graph capture; a captured call takes one
 # of its own from the graph's memory, whose counters the graph zeroes, so that
 # graphs replayed at the same time, and eager calls beside them, share nothing.
-_ATTN_COUNTERS = 2048
+_ATTN_COUNTERS = 4096
 _attn_ws: dict = {}
 
 

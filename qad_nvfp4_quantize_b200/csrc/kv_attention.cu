@@ -570,7 +570,9 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
   }
 }
 
-constexpr int kCounters = 2 * kMaxAttnCtas;  // of works, then of runs of kJoin parts
+// Counters of works, from kMaxAttnCtas on those of runs of kJoin parts; the 4,096 bytes that callers zero-fill.
+constexpr int kCounters = 1024;
+static_assert(2 * kMaxAttnCtas <= kCounters, "counters");
 constexpr int kPartFloats = 16 * (128 + 2);
 
 size_t kv_attention_workspace_bytes() {

@@ -204,6 +204,30 @@ def test_attention_strided_queries_long_context_many_sequences(nv, max_q):
     check(nv, rng, 64, 16, 4, 1, new, [x + 5 for x in new], max_q=max_q)
 
 
+@pytest.mark.parametrize("D,hq,heads,lens,window", [
+    (128, 8, 1, [41003], 0),             # one work over every block of the launch: runs of parts, then the runs
+    (64, 8, 2, [30001, 17], 29000),      # long and short works side by side
+    (128, 16, 1, [9000, 1, 12345], 0),   # 16 rows a KV head
+    (64, 5, 1, [70000], 700),            # a window far behind the start
+])
+def test_attention_joins_many_parts(nv, D, hq, heads, lens, window):
+    # a fresh workspace from memory that is not zero: only what the interface names is zero-filled
+    size = nv.lib().nvfp4_paged_attention_workspace_bytes()
+    nv._attn_ws.clear()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    dirt = [torch.full((size,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    del dirt
+    check(nv, np.random.default_rng(11), D, 64, hq, heads, [1] * len(lens), lens, window=window, max_q=1)
+
+
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_attention_more_new_tokens_than_cached_ones(nv, max_q):
+    # tokens before position 0 see nothing of a causal mask; without one they see all, or what their window reaches
+    for causal, window in ((True, 0), (True, 2), (False, 0), (False, 3)):
+        check(nv, np.random.default_rng(3), 64, 16, 4, 2, [5, 3, 40], [2, 0, 21], causal, window, max_q=max_q)
+
+
 def setup(nv, rng, D=128, page=16, hq=8, heads=2, new=(2, 1), lens=(90, 35)):
     table, P = tables(rng, lens, page)
     pages = random_pages(rng, P, heads, page, D)
