@@ -424,7 +424,8 @@ def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int, k_g: 
 
 # The calls below are short on the GPU (some microseconds), so their checks and
 # look-ups are kept cheap on the host: device indices instead of device objects,
-# raw stream handles, no context manager unless another device is current.
+# raw stream handles, no context manager unless another device is current, results
+# from new_empty (1.9 us; torch.empty with a device object takes 4.2).
 _INT32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
 
 
@@ -541,7 +542,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     seqs = (_ints(cu_q, "cu_q", index, batch + 1), _ints(kv_len, "kv_len", index, batch), batch,
             _ints(block_table, "block_table", index, batch, width), width)
     if out is None:
-        out = torch.empty((total, hq, dim), dtype=_BF16, device=q.device)
+        out = q.new_empty((total, hq, dim))
     elif out.shape != q.shape or out.dtype is not _BF16 or out.get_device() != index or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous torch.bfloat16 {list(q.shape)} tensor on cuda:{index}")
     if lse_out is not None:
@@ -549,7 +550,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
                 not lse_out.is_contiguous():
             raise ValueError(f"lse_out must be a contiguous torch.float32 [{total}, {hq}] tensor on cuda:{index}")
     elif want_lse:
-        lse_out = torch.empty((total, hq), dtype=_F32, device=q.device)
+        lse_out = q.new_empty((total, hq), dtype=_F32)
     if max_q is None:
         max_q = 1 if total <= batch else 0
     ws, ws_bytes, _keep, _ = _attention_workspace(index)
@@ -614,7 +615,7 @@ def kv_compact(refs: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Ten
     nbytes = int(lib().nvfp4_kv_compact_workspace_bytes(pages))
     # the moves, the count and the workspace (16-byte aligned) from one allocation
     at = 2 * cap + 4 + (-2 * cap) % 4
-    got = torch.empty(at + nbytes // 4 + 1, dtype=_INT32, device=refs.device)
+    got = refs.new_empty(at + nbytes // 4 + 1)
     src, dst, live = got[:cap], got[cap:2 * cap], got[2 * cap:2 * cap + 1]
     base = got.data_ptr()
     _call("nvfp4_kv_compact", index, *pool, _ints(refs_out, "refs_out", index, pages),
