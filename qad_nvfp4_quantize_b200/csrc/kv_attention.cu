@@ -10,7 +10,7 @@
 // Bound: HBM, 18*D bytes per 16 tokens and KV head. The rows of one KV head
 // (all its query heads, all new tokens of the tile) share each fetched granule.
 // Measured, D = 128, 8 rows: 64 sequences of up to 16,384 tokens (739 MB) in
-// 160 us, 4.6 TB/s; 2 of 131,072 (75 MB) in 35 us. Memory is 70 % busy then,
+// 154 us, 4.8 TB/s; 2 of 131,072 (75 MB) in 35 us. Memory is 70 % busy then,
 // issue slots 60 %, the ALU 50 %: what is left is dequantization, 256 of the
 // 640 instructions that a warp issues for 32 tokens. Single tokens over 1,024
 // cached ones take 14 us, 4 of them for lengths, page table and queries, one
@@ -47,7 +47,6 @@ constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kLongUnit = 384, kHeadUnits = 60;
 constexpr int kMaxAttnCtas = 320;
 constexpr int kJoin = 16;  // parts joined at a time
-static_assert(kMaxAttnCtas / kJoin >= kJoin && kMaxAttnCtas % kJoin == 0, "space for the parts that are joined");
 
 // Two CTAs for each SM where 128 registers a thread hold the output and the
 // queries: 16 rows of 128 dimensions need 230 (with 128 and spills, 16 rows over
@@ -63,7 +62,6 @@ struct AttnShared {
   union {
     uint8_t ring[kAttnWarps][kStages][2 * granule_bytes(D)];
     float join[kAttnWarps][kRows][kPad];
-    float parts[2][kMaxAttnCtas / kJoin][kRows];
     PartScratch scratch;
   };
   Part<8 * NT> part;
@@ -455,112 +453,111 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
     __syncthreads();
 
     // ---- a whole work is written out; a part goes to the workspace, and the last part joins them
-    auto write_rows = [&](auto&& value) {  // value(row, d) = unnormalised sums of 4 dimensions; sh.m, sh.l as joined
+    struct Sums {
+      float4 o;  // unnormalised, of 4 dimensions of a row
+      float m, l;
+    };
+    auto for_each = [&](auto&& f) {  // f(row, d): this thread's runs of 4 dimensions
 #pragma unroll
       for (int e0 = 0; e0 < kRows * (D / 4); e0 += kAttnThreads) {
-        const int e = e0 + tid, row = e / (D / 4), d = (e % (D / 4)) * 4;
-        const int32_t r = tile * kRows + row;
-        if (r >= nrows || (kRows * (D / 4) < kAttnThreads && e >= kRows * (D / 4))) continue;
-        const int32_t tok = a.by_group.divide(r), hq = head * a.group + r - tok * a.group;
-        const int64_t at = (seq.row0 + tok) * a.ix.hkv * a.group + hq;
-        const float lt = sh.l[row];
-        const float f = lt == 0.0f ? 0.0f : kValueScale * vg / lt;  // no visible token: zeros
-        const float4 x = value(row, d);
-        if (!NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status)) continue;
-        *reinterpret_cast<uint2*>(a.out + at * D + d) =
-            make_uint2(f32x2_to_bf16x2(x.x * f, x.y * f), f32x2_to_bf16x2(x.z * f, x.w * f));
-        if (a.lse && d == 0) a.lse[at] = lt == 0.0f ? -INFINITY : (sh.m[row] + log2f(lt)) * kLn2;
+        const int e = e0 + tid;
+        if (kRows * (D / 4) >= kAttnThreads || e < kRows * (D / 4)) f(e / (D / 4), (e % (D / 4)) * 4);
       }
     };
-    auto joined = [&](int row, int d) {
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto write_out = [&](int row, int d, const Sums& x) {
+      const int32_t r = tile * kRows + row;
+      if (r >= nrows) return;
+      const int32_t tok = a.by_group.divide(r), hq = head * a.group + r - tok * a.group;
+      const int64_t at = (seq.row0 + tok) * a.ix.hkv * a.group + hq;
+      const float f = x.l == 0.0f ? 0.0f : kValueScale * vg / x.l;  // no visible token: zeros
+      if (!NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status)) return;
+      *reinterpret_cast<uint2*>(a.out + at * D + d) =
+          make_uint2(f32x2_to_bf16x2(x.o.x * f, x.o.y * f), f32x2_to_bf16x2(x.o.z * f, x.o.w * f));
+      if (a.lse && d == 0) a.lse[at] = x.l == 0.0f ? -INFINITY : (x.m + log2f(x.l)) * kLn2;
+    };
+    constexpr int kPart = kRows * (D + 2);  // O, then m and l of each row
+    auto write_part = [&](float* part, int row, int d, const Sums& x) {
+      *reinterpret_cast<float4*>(part + row * D + d) = x.o;
+      if (d == 0) {
+        part[kRows * D + row] = x.m;
+        part[kRows * D + kRows + row] = x.l;
+      }
+    };
+    auto of_warps = [&](int row, int d) {
+      Sums x{make_float4(0.0f, 0.0f, 0.0f, 0.0f), sh.m[row], sh.l[row]};
 #pragma unroll
       for (int w2 = 0; w2 < kAttnWarps; ++w2) {
         const float4 y = *reinterpret_cast<const float4*>(&sh.join[w2][row][d]);
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
+        x.o.x += y.x;
+        x.o.y += y.y;
+        x.o.z += y.z;
+        x.o.w += y.w;
       }
       return x;
     };
-    constexpr int kPart = kRows * (D + 2);  // O, then m and l of each row
-    auto write_part = [&](float* part, auto&& value) {
-      for (int e = tid; e < kRows * (D / 4); e += kAttnThreads) {
-        const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-        *reinterpret_cast<float4*>(part + row * D + d) = value(row, d);
-      }
-      if (tid < kRows) {
-        part[kRows * D + tid] = sh.m[tid];
-        part[kRows * D + kRows + tid] = sh.l[tid];
-      }
-    };
     if (whole_work) {
-      write_rows(joined);
+      for_each([&](int row, int d) { write_out(row, d, of_warps(row, d)); });
     } else {
-      write_part(a.partial + (2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0)) * kPart, joined);
+      // A CTA has two places: the second for the part that begins a work, the first for a later part of one.
+      auto place = [&](int cta, int which) { return a.partial + (2 * (int64_t)cta + which) * kPart; };
+      float* part = place(blockIdx.x, unit0 == 0 ? 1 : 0);
+      for_each([&](int row, int d) { write_part(part, row, d, of_warps(row, d)); });
       __syncthreads();
       const int c0 = (int)(w.w0 / per), np = (int)((w.w0 + w.n - 1) / per) - c0 + 1;  // the CTAs that share the work
+      // What a run of parts from `first` on is joined to: the second place of a CTA that has this work only.
+      auto joined = [&](int first) { return place(c0 + (first > 0 ? first : 1), 1); };
       for (int round = np > kJoin ? 0 : 1; round < 2; ++round) {
-        const int stride = round == 1 && np > kJoin ? kJoin : 1, first = round == 0 ? ((int)blockIdx.x - c0) / kJoin * kJoin : 0;
-        const int n = round == 0 ? min(kJoin, np - first) : (np + stride - 1) / stride;
+        const bool runs = round == 1 && np > kJoin;
+        const int first = round == 0 ? ((int)blockIdx.x - c0) / kJoin * kJoin : 0;
+        const int n = round == 0 ? min(kJoin, np - first) : runs ? (np + kJoin - 1) / kJoin : np;
         if (n == 1) continue;  // a run of one part is joined already
         if (tid == 0) sh.last = arrive_last(a.counters + (round == 0 ? kMaxAttnCtas : 0) + c0 + first, n - 1);
         __syncthreads();
         if (!sh.last) break;
-        // m and l of the parts, then the factors 2^(m_c - m), then O with eight parts' loads in flight
-        float *ms = &sh.parts[0][0][0], *ls = &sh.parts[1][0][0];  // [n][kRows]; ms becomes the factors
-        auto part_of = [&](int c) { return a.partial + (2 * (int64_t)(c0 + c) + (c == 0 ? 1 : 0)) * kPart; };
-        for (int x = tid; x < n * kRows; x += kAttnThreads) {
-          const float* p = part_of(first + x / kRows * stride) + kRows * D + x % kRows;
-          ms[x] = __ldcg(p);
-          ls[x] = __ldcg(p + kRows);
-        }
-        __syncthreads();
-        for (int row = warp; row < kRows; row += kAttnWarps) {
-          float mt = -INFINITY, lt = 0.0f;
-          for (int c = lane; c < n; c += 32) mt = fmaxf(mt, ms[c * kRows + row]);
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, x));
-          for (int c = lane; c < n; c += 32) {
-            const float mc = ms[c * kRows + row];
-            const float f = mc == -INFINITY ? 0.0f : ex2(mc - mt);
-            ms[c * kRows + row] = f;
-            lt += f == 0.0f ? 0.0f : ls[c * kRows + row] * f;
-          }
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, x);
-          if (lane == 0) {
-            sh.m[row] = mt;
-            sh.l[row] = lt;
-          }
-        }
-        __syncthreads();
-        auto sum = [&](int row, int d) {
-          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int i = 0; i < n; i += 8) {
-            float4 y[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              y[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (i + c < n)
-                y[c] = __ldcg(reinterpret_cast<const float4*>(part_of(first + (i + c) * stride) + row * D + d));
-            }
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float f = i + c < n ? ms[(i + c) * kRows + row] : 0.0f;
-              x.x += y[c].x * f;
-              x.y += y[c].y * f;
-              x.z += y[c].z * f;
-              x.w += y[c].w * f;
-            }
-          }
-          return x;
+        auto nth = [&](int i) -> const float* {
+          const int c = runs ? i * kJoin : first + i;
+          return runs && c + 1 < np ? joined(c) : place(c0 + c, c == 0 ? 1 : 0);
         };
-        if (round == 1)
-          write_rows(sum);
-        else
-          write_part(part_of(first), sum);  // each thread over what it alone has read; m and l after everyone
+        // All of kBatch parts in flight, joined with a running maximum in the parts' order. (Maxima first and sums behind a
+        // barrier: 64 sequences of up to 16,384 tokens took 158 us, not 154.)
+        for_each([&](int row, int d) {
+          constexpr int kBatch = 8;
+          Sums x{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
+          for (int i = 0; i < n; i += kBatch) {
+            Sums y[kBatch];
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c) {
+              y[c] = Sums{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
+              if (i + c < n) {
+                const float* from = nth(i + c);
+                y[c].o = __ldcg(reinterpret_cast<const float4*>(from + row * D + d));
+                y[c].m = __ldcg(from + kRows * D + row);
+                y[c].l = __ldcg(from + kRows * D + kRows + row);
+              }
+            }
+            float mt = x.m;
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c) mt = fmaxf(mt, y[c].m);
+            if (mt == -INFINITY) continue;  // no visible token so far
+            auto add = [&](Sums& to, const Sums& z) {
+              const float f = ex2(z.m - mt);  // 0 for a part without a visible token: its sums are zeros
+              to.o.x += z.o.x * f;
+              to.o.y += z.o.y * f;
+              to.o.z += z.o.z * f;
+              to.o.w += z.o.w * f;
+              to.l += z.l * f;
+            };
+            Sums z{make_float4(0.0f, 0.0f, 0.0f, 0.0f), mt, 0.0f};
+            add(z, x);
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c) add(z, y[c]);
+            x = z;
+          }
+          if (round == 1)
+            write_out(row, d, x);
+          else
+            write_part(joined(first), row, d, x);
+        });
         __syncthreads();
       }
     }
@@ -600,8 +597,8 @@ cudaError_t launch_kv_attention(AttnArgs a, int D, int64_t max_q, void* workspac
   a.counters = static_cast<int32_t*>(workspace);
   a.partial = reinterpret_cast<float*>(a.counters + kCounters);
   // Rows of a KV head: up to 8 a tile of 8, up to 32 tiles of 16, above tiles of 256 on tcgen05. Measured with 32
-  // sequences of 8,192 tokens, 4 KV heads of 128: 8 rows 51 us in a tile of 8 and 66 in one of 16; 16 rows 84, 66 and
-  // 122 us on tcgen05; 32 rows 139, 107 and 123; with 64 sequences of 512 tokens and 64 rows 131, 133 and 59.
+  // sequences of 8,192 tokens, 4 KV heads of 128: 8 rows 48 us in a tile of 8 and 64 in one of 16; 16 rows 84, 64 and
+  // 122 us on tcgen05; 32 rows 139, 105 and 123; with 64 sequences of 512 tokens and 64 rows 131, 133 and 57.
   if (max_q == 0 || max_q > 32 || max_q * a.group > 32) return launch_kv_prefill(a, D, num_sms, s);
   const bool one = max_q * a.group <= 8;
   if (D == 128) return one ? launch_rows<128, 1>(a, num_sms, s) : launch_rows<128, 2>(a, num_sms, s);
