@@ -10,11 +10,11 @@
 // Bound: HBM, 18*D bytes per 16 tokens and KV head. The rows of one KV head
 // (all its query heads, all new tokens of the tile) share each fetched granule.
 // Measured, D = 128, 8 rows: 64 sequences of up to 16,384 tokens (739 MB) in
-// 154 us, 4.8 TB/s; 2 of 131,072 (75 MB) in 35 us. Memory is 70 % busy then,
-// issue slots 60 %, the ALU 50 %: what is left is dequantization, 256 of the
-// 640 instructions that a warp issues for 32 tokens. Single tokens over 1,024
-// cached ones take 14 us, 4 of them for lengths, page table and queries, one
-// read behind the other, and 1 us for each 32 tokens of a warp.
+// 154 us, 4.8 TB/s; 2 of 131,072 (75 MB) in 35 us. The same loop without its
+// arithmetic, which only copies, takes 137 us, without dequantization 145; issue
+// slots are 62 % busy, the ALU 52 %. Single tokens over 1,024 cached ones take 14
+// us, 4 of them for lengths, page table and queries, one read behind the other,
+// and 1 us for each 32 tokens of a warp.
 //
 // Layout. S^T = K Q^T and O^T = V^T P^T with mma m16n8k16 (FP16 in, FP32 out):
 // tokens resp. head dimensions fill the 16 rows, so 8 query rows waste nothing
@@ -42,9 +42,7 @@ namespace nvfp4 {
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;
-// Of the work list (find_part), in granules: the longest run that is not cut, and what a piece of a work costs besides
-// its granules.
-constexpr int kLongUnit = 384, kHeadUnits = 60;
+constexpr int kLongUnit = 384;  // granules: the longest run that is not cut (find_part)
 constexpr int kMaxAttnCtas = 320;
 constexpr int kJoin = 16;  // parts joined at a time
 
@@ -53,6 +51,22 @@ constexpr int kJoin = 16;  // parts joined at a time
 // 2,048 cached tokens took 33 us instead of 25).
 template <int D, int NT>
 constexpr int kCtasPerSm = NT == 1 || D == 64 ? 2 : 1;
+
+// Costs of the work list in the time of a granule: 0.12 us where two CTAs share an
+// SM (0.065 where one has it), 0.08 us for 16 rows of 128 dimensions. A piece of a
+// work takes about 5 us besides, joining p pieces 1.5 us and 0.25 for each, or 9 us
+// in two rounds. Measured, one sequence, 8 KV heads, 8 rows: 2,048 tokens uncut
+// 18.5 us, in 4 pieces a head 14.4, in 16 16.4, in 26 18.4; 32,768 in 8 pieces 30.9,
+// in 37 26.6.
+template <int kPerSm>
+struct AttnCost {
+  static constexpr int kHead = kPerSm == 2 ? 40 : 60;
+  static constexpr float kSparse = kPerSm == 2 ? 0.54f : 1.0f;
+  static NVFP4_DEVINL float join(float pieces) {
+    const float granules = pieces <= kJoin ? 12.0f + 2.0f * pieces : 75.0f;
+    return kPerSm == 2 ? granules : 1.5f * granules;
+  }
+};
 
 template <int D, int NT>
 struct AttnShared {
@@ -111,7 +125,8 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
   fence_barrier_init();
 
   prefetch_inputs(a, D);
-  find_part<kRows, 1, kLongUnit, kHeadUnits, kAttnThreads>(a, sh.scratch, sh.part, 1.0f);
+  using Cost = AttnCost<kCtasPerSm<D, NT>>;
+  find_part<kRows, 1, kLongUnit, Cost::kHead, kAttnThreads, Cost>(a, sh.scratch, sh.part);
   const int64_t u0 = sh.part.u0, u1 = sh.part.u1, per = sh.part.per;
   if (u0 >= u1) return;
   WorkCursor<kRows> w = sh.part.cursor;

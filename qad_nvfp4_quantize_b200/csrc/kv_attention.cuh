@@ -240,30 +240,33 @@ struct Part {
 struct PartScratch {
   int64_t sums[4][kStoredSums];
   int64_t warp_total[4][32];
+  int32_t warp_longest[32];
   int32_t long_seq[kLongList];
   int32_t long_count;
 };
 
 // This CTA's part of the list, called by all kThreads threads. What a piece of a
 // work costs besides its granules (its queries, its pipeline's start, the warps'
-// meeting) is worth kHead units of kFine granules, and joining the pieces of a
-// cut work about as much again (measured); so units are chosen among
+// meeting) is worth kHead units of kFine granules, joining the pieces of a cut
+// work Cost::join(pieces) (both measured), and where few CTAs work a granule
+// costs Cost::kSparse; so units are chosen among
 //   kFine granules and kHead in front of a work: all CTAs take equally much;
 //   runs of kLong / 4 or kLong granules: short works are not cut;
-//   the longest run of which every CTA gets one, if there are few works: no CTA
-//   has the end of one work and the start of another.
+//   the run that suits best among those of which every CTA gets one, if there are
+//   few works: no CTA has the end of one work and the start of another.
 // A thread counts a sequence, a warp one of many tiles.
-template <int kRows, int kFine, int kLong, int kHead, int kThreads>
-NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& part, float join_cost) {
+template <int kRows, int kFine, int kLong, int kHead, int kThreads, class Cost>
+NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& part) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kMid = kLong / 4, kKinds = 3;
   constexpr int kUnit[3] = {kFine, kMid, kLong};
   constexpr int kHeads[3] = {kHead, 0, 0};
-  constexpr float kPieceCost = kHead, kCutCost = 1.5f * kHead;  // in units of kFine; join_cost for each piece joined
+  constexpr float kPieceCost = kHead;  // in units of kFine
   constexpr int kSums = kKinds + 1;  // the units of each kind, and the works
   struct Sums {
     int64_t of[kSums];
   };
+  int32_t longest = 0;  // granules of the longest work that this thread has counted
   auto count = [&](const KvSeq& s, int t0, int step) {
     Sums u{};
     const int tiles = tiles_of<kRows>(a, s);
@@ -272,6 +275,7 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
 #pragma unroll
       for (int k = 0; k < kKinds; ++k) u.of[k] += (int64_t)units_of(span, kUnit[k], kHeads[k]) * a.ix.hkv;
       u.of[kKinds] += a.ix.hkv;
+      longest = max(longest, span.n);
     }
     return u;
   };
@@ -338,6 +342,8 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
         }
     }
     warp_sum(sum);
+    longest = uniform(longest);
+    if (lane == 0) sh.warp_longest[warp] = longest;
     if (lane == 0)
 #pragma unroll
       for (int k = 0; k < kSums; ++k) sh.warp_total[k][warp] = sum.of[k];
@@ -349,6 +355,8 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
 #pragma unroll
       for (int k = 0; k < kSums; ++k) all.of[k] = lane < kThreads / 32 ? sh.warp_total[k][lane] : 0;
     warp_sum(all);
+    if (!few) longest = lane < kThreads / 32 ? sh.warp_longest[lane] : 0;
+    longest = uniform(longest);
     // (a 64-bit division takes as long as all the rest of this)
     auto parts = [&](int64_t total) {
       return total < (int64_t(1) << 30) ? (int64_t)a.by_grid.divide((int32_t)total + (int)gridDim.x - 1)
@@ -360,23 +368,34 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       const int64_t works = all.of[kKinds];
       const float granules = fmaxf((float)(all.of[0] - works * kHead), 1.0f);  // in units of kFine
       const float each = __fdividef(granules, (float)works), share = (float)parts(all.of[0]);
-      float best = share + kPieceCost + kCutCost + join_cost * __fdividef(each, share);
+      const float most = (float)longest * (1.0f / kFine);
+      // (a CTA may have the end of one work and the start of the next: half a piece more)
+      float best = share + 1.5f * kPieceCost + Cost::join(__fdividef(each + kPieceCost, share));
+      // CTAs up to this many lie on SMs of their own
+      const float sparse = (float)gridDim.x * (1.0f / 3.0f);
 #pragma unroll
       for (int k = 1; k < kKinds; ++k) {
-        const bool cut = all.of[k] > works;
-        const float takes =
-            (float)parts(all.of[k]) * (__fdividef(1.125f * granules, (float)all.of[k]) + kPieceCost +
-                                       (cut ? kCutCost + join_cost * __fdividef((float)all.of[k], (float)works) : 0.0f));
+        const float run = fminf((float)kUnit[k] / kFine, most), units = (float)all.of[k];
+        const float takes = (float)parts(all.of[k]) * (run * (units <= sparse ? Cost::kSparse : 1.0f) + kPieceCost +
+                                                       (all.of[k] > works ? Cost::join(__fdividef(units, (float)works)) : 0.0f));
         if (takes < best) {
           best = takes;
           kind = k;
         }
       }
-      if (few && 2 * works <= gridDim.x) {  // ceil(n / unit) over the works is at most granules / unit + works
-        const int run = (int)ceilf(__fdividef(granules, (float)((int)gridDim.x - (int)works))) + 1;
-        if ((float)run + kPieceCost + kCutCost + join_cost * __fdividef(each, (float)run) < best) {
+      if (few && 2 * works <= gridDim.x) {
+        // lane x: runs that cut a work into x + 1, or as many as there are CTAs for (ceil(n / unit) over the works is at
+        // most granules / unit + works)
+        const float least = ceilf(__fdividef(granules, (float)((int)gridDim.x - (int)works))) + 1.0f;
+        const float run = fmaxf(least, lane < 31 ? ceilf(__fdividef(each, (float)(lane + 1))) : 0.0f);
+        const float pieces = ceilf(__fdividef(each, run));
+        const float takes = run * (pieces * (float)works <= sparse ? Cost::kSparse : 1.0f) + kPieceCost +
+                            (run < most ? Cost::join(fmaxf(pieces, 2.0f)) : 0.0f);
+        const uint32_t least_of = __reduce_min_sync(0xFFFFFFFFu, __float_as_uint(takes));  // positive: ordered as integers
+        if (__uint_as_float(least_of) < best) {
+          const int src = __ffs(__ballot_sync(0xFFFFFFFFu, __float_as_uint(takes) == least_of)) - 1;
           kind = 3;
-          unit = run * kFine;
+          unit = (int)__shfl_sync(0xFFFFFFFFu, run, src) * kFine;
         }
       }
       if (kind) {

@@ -46,6 +46,12 @@ constexpr int kUnitGranules = kTileTokens / kGranule;
 // 673 us, one of eight 660, of six 651, of four 684, of two 751.
 constexpr int kPolyEvery = 6;
 
+// Of the work list (find_part), in tiles of 128 tokens.
+struct PreCost {
+  static constexpr float kSparse = 1.0f;
+  static NVFP4_DEVINL float join(float pieces) { return 3.0f + 0.5f * pieces; }
+};
+
 template <int D>
 struct PreShared {
   static constexpr int kStages = 3;  // tiles of codes in flight
@@ -261,7 +267,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     fence_barrier_init();
   }
   prefetch_inputs(a, D);
-  find_part<kPreRows, kUnitGranules, 16 * kUnitGranules, 2, kPreThreads>(a, sh.scratch, sh.part, 0.5f);
+  find_part<kPreRows, kUnitGranules, 16 * kUnitGranules, 2, kPreThreads, PreCost>(a, sh.scratch, sh.part);
   if (sh.part.u0 >= sh.part.u1) return;
   const int64_t u0 = sh.part.u0;
   WorkCursor<kPreRows>& w = sh.cursor[warp];
