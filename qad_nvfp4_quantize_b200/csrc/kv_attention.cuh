@@ -371,7 +371,8 @@ NVFP4_DEVINL void find_part(const AttnArgs& a, PartScratch& sh, Part<kRows>& par
       const float most = (float)longest * (1.0f / kFine);
       // (a CTA may have the end of one work and the start of the next: half a piece more)
       float best = share + 1.5f * kPieceCost + Cost::join(__fdividef(each + kPieceCost, share));
-      // CTAs up to this many lie on SMs of their own
+      // CTAs up to this many lie on SMs of their own. (Not half of the grid: six SMs of 148 take a second CTA as the
+      // launch's 103rd to 108th, before others have one; 128 CTAs took as long a granule as 296.)
       const float sparse = (float)gridDim.x * (1.0f / 3.0f);
 #pragma unroll
       for (int k = 1; k < kKinds; ++k) {
