@@ -336,7 +336,8 @@ nvfp4_status nvfp4_quantize_noalloc(const void* x, int64_t M, int64_t K, nvfp4_m
  *              low nibble of byte j), K block scales [16][D/16] (E4M3), V
  *              codes, V block scales. D = 64 or 128; page_size = 16, 32, 64 or
  *              128.
- * k_g, v_g     device FP32 scalars: static global scales of K and V.
+ * k_g, v_g     device FP32 scalars: static global scales of K and V (finite, not
+ *              negative).
  * block_table  [batch][table_width] int32: page j of sequence b.
  * cu_q         [batch + 1] int32, non-decreasing: rows [cu_q[b], cu_q[b+1]) of
  *              the new-token tensors belong to sequence b.
