@@ -478,14 +478,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         };
         const bool write = live && NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status);
         if (whole_work) {
-          const float f = l == 0.0f ? 0.0f : kValueScale * vg / l;
+          // (by the maximum: l of a row that saw nothing holds the 2^-126 that exp2_poly gives for a masked score)
+          const float f = m == -INFINITY ? 0.0f : kValueScale * vg / l;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_read32(t_o + 32 * c, o);
             if (write) write_row(c, reinterpret_cast<const float*>(o), f);
           }
-          if (write && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+          if (write && a.lse) a.lse[at] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
         } else {
           // part of a work: m, l, then O in pieces of 4 columns x 128 rows
           constexpr int kPart = 128 * (D + 2);

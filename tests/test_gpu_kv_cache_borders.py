@@ -1,0 +1,59 @@
+"""Paged NVFP4 KV cache on the GPU at the borders of what its interface allows."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv_oracle as kv
+from tests.test_gpu_kv_cache import compare, cumulative, ints, queries, random_pages, scalars, tables
+from tests.util import bf16_np, require_gpu, to_np
+
+pytestmark = pytest.mark.gpu
+
+KG = 0.11                    # global scale of the random keys: values of about 1
+
+
+@pytest.fixture(scope="module")
+def nv():
+    return require_gpu()
+
+
+def problem(nv, rng, D, page, hq, heads, new, lens, vg):
+    """Random pages and queries under the value scale vg: what attention takes, and what the oracle takes."""
+    table, P = tables(rng, lens, page)
+    pages = random_pages(rng, P, heads, page, D)
+    q, qn = queries(rng, sum(new), hq, D)
+    cache = nv.KVCache(torch.from_numpy(pages).cuda(), *scalars(KG, vg), page, D)
+    return q, qn, cache, pages, table
+
+
+# ---------------------------------------------------- rows that see nothing
+@pytest.mark.parametrize("vg", [0.07, 0.3, 1.0, 4.0, 2.0 ** 100])
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_rows_that_see_nothing_are_zero_under_every_value_scale(nv, max_q, vg):
+    # no cached tokens; more new tokens than positions, before rows that see some; a window in front of what is there
+    for D, page, hq, heads, new, lens, causal, window in (
+            (64, 16, 4, 2, [2, 5, 1], [0, 3, 9], True, 0), (128, 16, 4, 2, [40, 3], [0, 1], True, 0),
+            (128, 16, 8, 2, [300, 1], [140, 0], True, 0), (64, 32, 6, 3, [70, 2], [64, 0], True, 5),
+            (128, 64, 2, 1, [1, 1], [0, 0], False, 0)):
+        q, qn, cache, pages, table = problem(nv, np.random.default_rng(sum(new)), D, page, hq, heads, new, lens, vg)
+        cu = cumulative(new)
+        out, lse = nv.paged_attention(q, cache, ints(table), ints(cu), ints(lens), causal=causal, window=window,
+                                      max_q=max_q, want_lse=True)
+        ref = kv.attention(qn, pages, table, cu, lens, KG, vg, page, D ** -0.5, causal, window)
+        none = ref["seen"] == 0
+        assert none.any() and not bf16_np(out)[none].any() and np.isneginf(to_np(lse)[none]).all()
+        compare(out, lse, ref, D)
+        assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("vg", [0.07, 4.0])
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_rows_without_a_page_are_zero(nv, max_q, vg):
+    # every page outside the pool: nothing to see, in short works and in one that is cut into parts
+    for lens in ([35, 1], [30000, 5]):
+        q, _, cache, _, table = problem(nv, np.random.default_rng(3), 128, 64, 8, 2, [2, 1], lens, vg)
+        for page in (-1, cache.pages.shape[0]):
+            out, lse = nv.paged_attention(q, cache, ints(np.full_like(table, page)), ints([0, 2, 3]), ints(lens),
+                                          max_q=max_q, want_lse=True)
+            assert not out.any() and torch.isneginf(lse).all()
+            assert nv.device_status() == 9
