@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          top[nt][c] = fmaxf(max3(s[nt][0][c], s[nt][0][c + 2], s[nt][1][c]), s[nt][1][c + 2]) * factor[nt][c];
-          grow |= top[nt][c] > m[nt][c] + kRescaleAt;
+          top[nt][c] = max2(max3(s[nt][0][c], s[nt][0][c + 2], s[nt][1][c]), s[nt][1][c + 2]) * factor[nt][c];
+          grow |= takes_new_max(top[nt][c], m[nt][c]);
         }
       if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
@@ -348,10 +348,10 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float mx = top[nt][c];
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-            const float m1 = fmaxf(m[nt][c], mx);
+            mx = max2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+            mx = max2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+            mx = max2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+            const float m1 = new_max(mx, m[nt][c]);
             const float f = m[nt][c] == kStartMax ? 0.0f : ex2(m[nt][c] - m1);
             m[nt][c] = m1;
             l[nt][c] *= f;
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
         const int row = 8 * nt + 2 * t + c;
         float mt = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) mt = fmaxf(mt, sh.wm[w][row]);
+        for (int w = 0; w < kAttnWarps; ++w) mt = max2(mt, sh.wm[w][row]);
         const float f = m[nt][c] == -INFINITY ? 0.0f : ex2(m[nt][c] - mt);
 #pragma unroll
         for (int j = 0; j < kSteps; ++j)  // dimensions 2j, 2j+1 of the run of D/8 that starts at g*D/8
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       }
     if (tid < kRows) {
       float mt = -INFINITY, lt = 0.0f;
-      for (int w = 0; w < kAttnWarps; ++w) mt = fmaxf(mt, sh.wm[w][tid]);
+      for (int w = 0; w < kAttnWarps; ++w) mt = max2(mt, sh.wm[w][tid]);
       for (int w = 0; w < kAttnWarps; ++w)
         lt += sh.wm[w][tid] == -INFINITY ? 0.0f : sh.wl[w][tid] * ex2(sh.wm[w][tid] - mt);
       sh.m[tid] = mt;
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
             }
             float mt = x.m;
 #pragma unroll
-            for (int c = 0; c < kBatch; ++c) mt = fmaxf(mt, y[c].m);
+            for (int c = 0; c < kBatch; ++c) mt = max2(mt, y[c].m);
             if (mt == -INFINITY) continue;  // no visible token so far
             auto add = [&](Sums& to, const Sums& z) {
               const float f = ex2(z.m - mt);  // 0 for a part without a visible token: its sums are zeros

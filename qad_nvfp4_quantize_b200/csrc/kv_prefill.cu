@@ -405,9 +405,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
             t2 = max3(t2, __uint_as_float(y[e + 4]), __uint_as_float(y[e + 5]));
             t3 = max3(t3, __uint_as_float(y[e + 6]), __uint_as_float(y[e + 7]));
           }
-          const float top = max3(fmaxf(t0, t1), t2, t3) * factor;
-          if (__any_sync(0xFFFFFFFFu, top > m + kRescaleAt)) {
-            const float m1 = fmaxf(m, top);
+          const float top = max3(max2(t0, t1), t2, t3) * factor;
+          if (__any_sync(0xFFFFFFFFu, takes_new_max(top, m))) {
+            const float m1 = new_max(top, m);
             const float f = m == kStartMax ? 0.0f : ex2(m - m1);
             m = m1;
             l *= f;
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           if (!(ok = meet())) break;
           if (sh.last[i]) {
             float mt = -INFINITY, lt = 0.0f;
-            for (int64_t c = c0; c <= c1; ++c) mt = fmaxf(mt, __ldcg(part_of(c, c == c0) + row));
+            for (int64_t c = c0; c <= c1; ++c) mt = max2(mt, __ldcg(part_of(c, c == c0) + row));
             for (int64_t c = c0; c <= c1; ++c) {
               const float mc = __ldcg(part_of(c, c == c0) + row);
               lt += mc == -INFINITY ? 0.0f : __ldcg(part_of(c, c == c0) + 128 + row) * ex2(mc - mt);

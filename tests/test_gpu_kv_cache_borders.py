@@ -57,3 +57,55 @@ def test_rows_without_a_page_are_zero(nv, max_q, vg):
                                           max_q=max_q, want_lse=True)
             assert not out.any() and torch.isneginf(lse).all()
             assert nv.device_status() == 9
+
+
+# ------------------------------------------------------- non-finite queries
+@pytest.mark.parametrize("lens", [(90, 35), (9000, 700), (100000, 60000)])
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_non_finite_queries_give_nan_whether_their_work_is_cut_or_not(nv, max_q, lens):
+    q, _, cache, _, table = problem(nv, np.random.default_rng(lens[0]), 128, 64, 8, 2, [3, 1], lens, 0.07)
+    args = (ints(table), ints([0, 3, 4]), ints(lens))
+    want, lse0 = nv.paged_attention(q, cache, *args, max_q=max_q, want_lse=True)
+    assert torch.isfinite(want.float()).all() and torch.isfinite(lse0).all()
+    rows = [(0, 1), (1, 3), (3, 0), (2, 7)]
+    for value in (float("nan"), float("inf"), -float("inf")):
+        bad = q.clone()
+        for t, h in rows:
+            bad[t, h, 5 * h % 128] = value       # (among so many keys one has the value's sign there: its score is +Inf)
+        out, lse = nv.paged_attention(bad, cache, *args, max_q=max_q, want_lse=True)
+        for t, h in rows:
+            assert torch.isnan(out[t, h]).all() and torch.isnan(lse[t, h]), (value, t, h)
+            out[t, h], lse[t, h] = want[t, h], lse0[t, h]
+        assert torch.equal(out, want) and torch.equal(lse, lse0)      # the other rows: bit for bit
+    assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_nan_queries_that_see_one_or_two_tokens(nv, max_q, D):
+    # each place of a 64-token step by itself, under windows of one and two tokens
+    lens = list(range(1, 81))
+    q, _, cache, _, table = problem(nv, np.random.default_rng(D), D, 32, 2, 2, [1] * 80, lens, 0.07)
+    bad = q.clone()
+    bad[:, 0] = float("nan")
+    for window in (1, 2):
+        args = (ints(table), ints(range(81)), ints(lens))
+        want, _ = nv.paged_attention(q, cache, *args, window=window, max_q=max_q)
+        out, lse = nv.paged_attention(bad, cache, *args, window=window, max_q=max_q, want_lse=True)
+        assert torch.isnan(out[:, 0]).all() and torch.isnan(lse[:, 0]).all()
+        assert torch.equal(out[:, 1], want[:, 1])
+
+
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_scores_of_minus_infinity_weigh_nothing(nv, max_q):
+    # A query of -Inf in one dimension, keys that are positive there: every score is -Inf, the sum of their weights 0.
+    D, page, n = 64, 16, 50
+    k = torch.ones((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    cache = nv.kv_cache(4, 1, D, page, *scalars(0.001, 0.001))
+    table = ints([[0, 1, 2, 3]])
+    nv.kv_append(cache, k, k, table, ints([0, n]), ints([n]))
+    q = torch.ones((1, 2, D), dtype=torch.bfloat16, device="cuda")
+    q[0, 1, 7] = -float("inf")
+    out, lse = nv.paged_attention(q, cache, table, ints([0, 1]), ints([n]), max_q=max_q, want_lse=True)
+    assert not out[0, 1].any() and torch.isneginf(lse[0, 1])
+    assert torch.isfinite(lse[0, 0]) and out[0, 0].all()
