@@ -114,14 +114,14 @@ def attention_tolerance(ref, D):
     A score's error: D products of exact FP16 operands summed in FP32, in any order, (D + 8) half steps of 2^-24 of
     `reach` (the query's own FP16 rounding, 2^-29 of its row's largest, is far inside 8 of them for D <= 128: D * 2^-29
     <= 4 * 2^-24), then two factors and the difference s - m at 2^-24 each of at most 2 * reach; the 2^x function 2^-22.
-    A weight p is rounded to FP16: 2^-11 of itself, or 2^-25 absolutely below 2^-14, with the largest p at least 1 in
-    the running scale. The sums over tokens add (seen + 64) * 2^-24, the output is rounded to BF16: 2^-8 (half of
+    A weight p is rounded to FP16: 2^-11 of itself, or 2^-25 absolutely below 2^-14, with the largest p at least 2^7 in
+    the running scale: 2^-32 of it. The sums over tokens add (seen + 64) * 2^-24, the output is rounded to BF16: 2^-8 (half of
     eps = 2^-7)."""
     e_s = (D + 16) * 2.0 ** -24 * ref["reach"] + 2.0 ** -21
     e_sum = (ref["seen"] + 64) * 2.0 ** -24
     rel = 2 * e_s + 2.0 ** -11 + 2 * e_sum
     out = 2.0 ** -8 * np.abs(ref["out"]) + rel[..., None] * ref["mass"] * (1 + 2.0 ** -8) \
-        + (ref["seen"] * ref["big"] * 2.0 ** -25)[..., None]
+        + (ref["seen"] * ref["big"] * 2.0 ** -32)[..., None]
     lse = e_s + e_sum + 2.0 ** -22 * (np.abs(np.where(np.isfinite(ref["lse"]), ref["lse"], 0.0)) + ref["reach"] + 1)
     return out, lse
 

@@ -3,9 +3,10 @@
 //
 // Mathematics: one pass over the cached tokens with a running maximum m, sum l
 // and unnormalised output O per query row: m' = max(m, s), O = O * 2^(m - m') +
-// 2^(s - m') v (scores in units of log2). O and l are rescaled only when a
-// score exceeds m by more than 8, so p = 2^(s - m) stays below 2^8 and the sum
-// in FP32 loses nothing.
+// 2^(s - m') v (scores in units of log2). m is held 7 below the score that set
+// it, and O and l are rescaled only when a score exceeds m by more than 15: a
+// row's largest p = 2^(s - m) lies between 2^7 and 2^15, FP16's upper end, and
+// the sums in FP32 lose nothing.
 //
 // Bound: HBM, 18*D bytes per 16 tokens and KV head. The rows of one KV head
 // (all its query heads, all new tokens of the tile) share each fetched granule.
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
             }
           }
       }
-      // P^T as B fragments: FP16 rounds p to 2^-11 of itself
+      // P^T as B fragments: FP16 rounds p to 2^-11 of itself from 2^-14 on, below to 2^-25 (2^-32 of the largest p)
       uint32_t pf[NT][2][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {

@@ -133,17 +133,21 @@ NVFP4_DEVINL int arrive_last(int32_t* counter, int others) {
 }
 
 constexpr int64_t kAttnWaitCycles = 4000000000ll;  // bound of every wait, about 2 s
-constexpr float kRescaleAt = 8.0f;                // lag of the running maximum, in log2 units
+// The running maximum m of a row is held kHeadroom below the score that set it (in log2 units) and may lag kRescaleAt
+// behind a larger one, so a row's largest weight 2^(s - m) lies in [2^7, 2^15]: weights are FP16 operands, which hold
+// 11 bits down to 2^-14 and multiples of 2^-24 below. Without the head-room tokens 16 nats below an attention sink lost
+// their weights, and those more than 17.3 below it vanished from the output.
+constexpr float kRescaleAt = 8.0f, kHeadroom = 7.0f;
 constexpr float kStartMax = -1e30f;                // running maximum before the first visible token
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 // A row whose largest new score is `top` keeps its running maximum m (so that
 // its neighbours do not change its result) or takes a new one: where top exceeds
-// m by more than the lag, or either is NaN. A score of +Inf has no softmax: NaN too.
-NVFP4_DEVINL bool takes_new_max(float top, float m) { return !(top <= m + kRescaleAt); }
+// m by more than head-room and lag, or either is NaN. A score of +Inf has no softmax: NaN too.
+NVFP4_DEVINL bool takes_new_max(float top, float m) { return !(top <= m + (kRescaleAt + kHeadroom)); }
 NVFP4_DEVINL float new_max(float top, float m) {
   if (!takes_new_max(top, m)) return m;
-  return top == INFINITY ? NAN : max2(top, m);
+  return top == INFINITY ? NAN : max2(top - kHeadroom, m);
 }
 
 // The same value in every lane, in a form that the compiler knows to be uniform.

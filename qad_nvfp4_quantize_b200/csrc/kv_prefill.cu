@@ -29,9 +29,10 @@
 // P V and the next S each time (4,096 over 12,288: 741 us). Two row tiles, not
 // one, because each dequantized tile then serves 256 rows.
 //
-// The running maximum m is allowed to lag by 8 (in log2 units): a row takes a
-// new one, and O is rescaled, only when a score exceeds it by more, so that p
-// stays below 2^8 and most steps leave O alone.
+// The running maximum m is held 7 below the score that set it and may lag by 8
+// (in log2 units): a row takes a new one, and O is rescaled, only when a score
+// exceeds m by more than 15, so that p stays within FP16 and most steps leave O
+// alone.
 #include <cuda_fp16.h>
 
 #include "kv_attention.cuh"
@@ -202,7 +203,7 @@ NVFP4_DEVINL f32x2 add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 2^x of two numbers x < 128 on the FMA pipe: n = x rounded to an integer (by
+// 2^x of two numbers x < 128 (x <= 15 here) on the FMA pipe: n = x rounded to an integer (by
 // adding 1.5 * 2^23), a polynomial for 2^(x - n) on [-1/2, 1/2], n added to the
 // exponent. Its coefficients are a relative minimax fit of degree 5 (least
 // squares, reweighted): off by at most 2^-22 when evaluated in FP32. Arguments
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
               }
             }
           }
-          // p as FP16 pairs (to 2^-11 of itself) into the first half of the buffer
+          // p as FP16 pairs (to 2^-11 of itself from 2^-14 on, below to 2^-25) into the first half of the buffer
           f32x2 sum = 0;
           const f32x2 ff = pack2(factor, factor), mm = pack2(-m, -m);
 #pragma unroll

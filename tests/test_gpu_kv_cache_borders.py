@@ -109,3 +109,32 @@ def test_scores_of_minus_infinity_weigh_nothing(nv, max_q):
     out, lse = nv.paged_attention(q, cache, table, ints([0, 1]), ints([n]), max_q=max_q, want_lse=True)
     assert not out[0, 1].any() and torch.isneginf(lse[0, 1])
     assert torch.isfinite(lse[0, 0]) and out[0, 0].all()
+
+
+# ------------------------------------------------------------ attention sinks
+@pytest.mark.parametrize("nats", [12.0, 14.0, 16.0, 18.0])
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_tokens_behind_an_attention_sink_keep_their_weights(nv, max_q, nats):
+    """The first token far above all others, with values of zero: the output is what the others' small weights bring. As
+    many works as the card holds CTAs, so that a row's tokens are not divided and its state has the sink in it."""
+    D, page, heads, hq, L, seqs = 128, 64, 8, 16, 4096, 37
+    rng = np.random.default_rng(int(nats))
+    sign = np.where(rng.random((heads, D)) < 0.5, -1.0, 1.0)
+    k = rng.standard_normal((L, heads, D)) * 0.05
+    k[0] = sign * nats / D ** 0.5                      # scale * q . k = nats, for a query of the signs
+    v = rng.uniform(0.5, 1.0, (L, heads, D))
+    v[0] = 0.0
+    k, v = (torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).cuda() for x in (k, v))
+    kg, vg = 0.001, 0.0005                              # keys to 2.6, values to 1.3
+    cache = nv.kv_cache(L // page, heads, D, page, *scalars(kg, vg))
+    row = rng.permutation(L // page)
+    nv.kv_append(cache, k, v, ints(row[None]), ints([0, L]), ints([L]))
+    q = torch.from_numpy(np.repeat(sign, hq // heads, 0)[None].astype(np.float32)).to(torch.bfloat16)
+    ref = kv.attention(bf16_np(q), to_np(cache.pages), row[None], [0, 1], [L], kg, vg, page, D ** -0.5, True, 0)
+    # (the sink's key is a multiple of its block scale, which rounds by at most 2^-4 of itself)
+    assert (ref["out"] > 0).all() and (ref["out"] < np.exp(0.5 - nats * (1 - 2.0 ** -4)) * L).all()
+    out, _ = nv.paged_attention(q.cuda().repeat(seqs, 1, 1), cache, ints(np.repeat(row[None], seqs, 0)),
+                                ints(range(seqs + 1)), ints([L] * seqs), max_q=max_q)
+    err = np.abs(bf16_np(out).astype(np.float64) - ref["out"])
+    tol, _ = kv.attention_tolerance(ref, D)
+    assert (err <= tol).all(), float((err / tol).max())
