@@ -347,7 +347,8 @@ nvfp4_status nvfp4_quantize_noalloc(const void* x, int64_t M, int64_t K, nvfp4_m
  * captured graph can be replayed with other values. A negative, decreasing or
  * too large offset or length, or a page outside the pool, is recorded as
  * NVFP4_ERR_PAGE and its tokens are skipped (appending) or masked (attention).
- * Rows at or behind cu_q[batch] are neither read nor written.
+ * Rows before cu_q[0] and at or behind cu_q[batch] belong to no sequence: their
+ * results are not written.
  */
 
 /* Bytes of one head's part of a page; 0 for an unsupported size. Host only. */

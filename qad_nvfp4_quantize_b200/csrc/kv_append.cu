@@ -69,10 +69,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(
       placed = t0;
       while (b + 1 < ix.batch && t0 >= (int64_t)ix.cu[b + 1]) seq = kv_sequence(ix, ++b, status);
       const int64_t i = t0 - seq.row0, pos = (int64_t)seq.len - seq.rows + i;
-      // (a sequence longer than its cache: no such position)
-      int64_t page = i < 0 || i >= seq.rows || pos < 0 ? -1 : ix.table[(int64_t)b * ix.width + (pos >> pshift)];
+      // (rows before cu[0] belong to nobody, those of malformed offsets are recorded with these; a sequence longer than its
+      // cache has no such position)
+      const bool owned = i >= 0 && i < seq.rows;
+      int64_t page = !owned || pos < 0 ? -1 : ix.table[(int64_t)b * ix.width + (pos >> pshift)];
       if (page >= ix.num_pages) page = -1;
-      if (page < 0) record_status(status, NVFP4_ERR_PAGE);
+      if (owned && page < 0) record_status(status, NVFP4_ERR_PAGE);
       const int slot = (int)pos & (ix.page - 1), row = slot % kGranule;
       base = page < 0 ? nullptr
                       : pages + ((page * ix.hkv << gshift) + slot / kGranule) * granule_bytes(D) + (is_v ? 9 * D : 0) +

@@ -138,3 +138,23 @@ def test_tokens_behind_an_attention_sink_keep_their_weights(nv, max_q, nats):
     err = np.abs(bf16_np(out).astype(np.float64) - ref["out"])
     tol, _ = kv.attention_tolerance(ref, D)
     assert (err <= tol).all(), float((err / tol).max())
+
+
+# -------------------------------------------- a batch that begins behind row 0
+@pytest.mark.parametrize("mode", ["max", "four_over_six"])
+def test_append_of_the_last_sequences_of_a_batch(nv, mode):
+    """Offsets that begin above 0 (the last sequences of a larger batch over the same rows): the rows before them belong
+    to nobody, which is no error."""
+    rng = np.random.default_rng(5)
+    D, page, heads, new, lens = 64, 16, 2, [40, 7, 1, 20], [40, 30, 16, 21]
+    table, P = tables(rng, lens, page)
+    x = torch.from_numpy(rng.standard_normal((2, sum(new), heads, D)).astype(np.float32)).to(torch.bfloat16)
+    pages = rng.integers(0, 256, (P, heads, nv.kv_page_bytes(page, D)), dtype=np.uint8)
+    for first in range(4):
+        cache = nv.KVCache(torch.from_numpy(pages).cuda(), *scalars(0.002, 0.003), page, D)
+        cu = cumulative(new)[first:]
+        nv.kv_append(cache, x[0].cuda(), x[1].cuda(), ints(table[first:]), ints(cu), ints(lens[first:]), mode=mode)
+        assert nv.device_status() == 0, first
+        ref = pages.copy()
+        kv.append(ref, bf16_np(x[0]), bf16_np(x[1]), table[first:], cu, lens[first:], 0.002, 0.003, page, mode)
+        assert np.array_equal(to_np(cache.pages), ref)
