@@ -26,6 +26,10 @@ template <int D, bool kFos, bool kTable>
 __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(
     const uint4* __restrict__ k, const uint4* __restrict__ v, int64_t stride8, KvIndex ix, uint8_t* pages,
     const float* __restrict__ k_g, const float* __restrict__ v_g, int64_t per_warp, int* status) {
+  if (blockIdx.x == gridDim.x - 1) {  // reports what is malformed, also where no row leads to it
+    for (int b = threadIdx.x; b < ix.batch; b += kAppendWarps * 32) kv_sequence(ix, b, status);
+    return;
+  }
   const int lane = threadIdx.x & 31;
   const bool is_v = blockIdx.x & 1;
   if (kTable) build_step_table(is_v ? *v_g : *k_g);
@@ -55,7 +59,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(
     if ((int64_t)ix.cu[mid + 1] > t) hi = mid; else lo = mid + 1;
   }
   int b = lo;
-  KvSeq seq = kv_sequence(ix, b, status);
+  KvSeq seq = kv_sequence(ix, b, nullptr);
   int64_t placed = -1;      // token that `base` belongs to
   uint8_t* base = nullptr;  // its K or V rows of head 0, null where it has no place
   while (t < t1) {
@@ -67,9 +71,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(
     if (t < t1) load_raw16(x, t * stride8 + 2 * n, NVFP4_IN_BOUNDS(2 * n + 1, stride8, status), next);
     if (t0 != placed) {
       placed = t0;
-      while (b + 1 < ix.batch && t0 >= (int64_t)ix.cu[b + 1]) seq = kv_sequence(ix, ++b, status);
+      while (b + 1 < ix.batch && t0 >= (int64_t)ix.cu[b + 1]) seq = kv_sequence(ix, ++b, nullptr);
       const int64_t i = t0 - seq.row0, pos = (int64_t)seq.len - seq.rows + i;
-      // (rows before cu[0] belong to nobody, those of malformed offsets are recorded with these; a sequence longer than its
+      // (rows before cu[0] belong to nobody; a sequence longer than its
       // cache has no such position)
       const bool owned = i >= 0 && i < seq.rows;
       int64_t page = !owned || pos < 0 ? -1 : ix.table[(int64_t)b * ix.width + (pos >> pshift)];
@@ -116,11 +120,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(
 cudaError_t launch_kv_append(const void* k, const void* v, int64_t stride, int D, const KvIndex& ix, uint8_t* pages,
                              const float* k_g, const float* v_g, bool fos, int* status, int num_sms, cudaStream_t s) {
   if (ix.total == 0 || ix.batch == 0) return cudaSuccess;
-  // a warp takes consecutive tokens; even CTAs quantize K, odd ones V
+  // a warp takes consecutive tokens; even CTAs quantize K, odd ones V, the last one checks the offsets and lengths
   const int64_t slots = (int64_t)num_sms * 32;
   const int64_t per_warp = (ix.total + slots - 1) / slots;
   const int64_t warps = (ix.total + per_warp - 1) / per_warp;
-  const int grid = 2 * (int)((warps + kAppendWarps - 1) / kAppendWarps);
+  const int grid = 2 * (int)((warps + kAppendWarps - 1) / kAppendWarps) + 1;
   // The table pays for itself where a warp quantizes several tokens twice: in FOUR_OVER_SIX, 8 KV heads of 128, 1 token
   // a warp takes 16.4 us without and 18.4 with it, 2 25.5 and 26.6, 4 42.0 and 41.0, 6 58.4 and 57.4; in MAX, 6 take
   // 38.9 and 40.0.

@@ -158,3 +158,17 @@ def test_append_of_the_last_sequences_of_a_batch(nv, mode):
         ref = pages.copy()
         kv.append(ref, bf16_np(x[0]), bf16_np(x[1]), table[first:], cu, lens[first:], 0.002, 0.003, page, mode)
         assert np.array_equal(to_np(cache.pages), ref)
+
+
+def test_append_reports_every_malformed_offset_and_length(nv):
+    """Offsets that decrease and lengths outside the table are reported however the rows are divided over the card, also
+    those of a sequence that no row leads to."""
+    D, page, n = 64, 16, 8
+    one = torch.ones((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    cache = nv.kv_cache(4, 1, D, page, *scalars(0.01, 0.01))
+    table = ints([[0], [1], [2]])
+    for cu, lens, status in (([0, 5, 5, 8], [5, 0, 3], 0), ([0, 5, 5, 8], [16, 16, 16], 0), ([0, 5, 3, 8], [5, 9, 9], 9),
+                             ([0, 5, 5, 8], [5, 17, 3], 9), ([0, 5, 5, 8], [5, -1, 3], 9), ([-1, 0, 5, 8], [1, 5, 3], 9),
+                             ([0, 5, 8, 9], [5, 3, 1], 9)):
+        nv.kv_append(cache, one, one, table, ints(cu), ints(lens))
+        assert nv.device_status() == status, (cu, lens)
