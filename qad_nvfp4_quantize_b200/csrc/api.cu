@@ -354,7 +354,8 @@ nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_stride, int64_t tota
   a.scale = scale;
   a.group = q_heads / kv_heads;
   a.causal = causal != 0;
-  a.window = window;
+  // no position exceeds 2^31: a window beyond that hides nothing, and position - window must not pass 64 bits
+  a.window = window < (int64_t(1) << 31) ? window : 0;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = d->status;

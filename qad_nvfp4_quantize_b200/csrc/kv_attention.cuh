@@ -113,7 +113,7 @@ struct AttnArgs {
   int group;           // query heads per KV head
   Divisor by_group, by_grid;
   int causal;
-  int64_t window;      // 0: no window
+  int64_t window;      // 0: no window; below 2^31
   uint16_t* out;       // BF16 [total][hq][D]
   float* lse;          // FP32 [total][hq] or null
   float* partial;      // workspace

@@ -172,3 +172,17 @@ def test_append_reports_every_malformed_offset_and_length(nv):
                              ([0, 5, 8, 9], [5, 3, 1], 9)):
         nv.kv_append(cache, one, one, table, ints(cu), ints(lens))
         assert nv.device_status() == status, (cu, lens)
+
+
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_a_window_of_any_size(nv, max_q):
+    # windows up to the type's largest value, with tokens before position 0: what no window gives, bit for bit
+    new, lens = [200, 40, 1], [100, 0, 77]
+    q, _, cache, _, table = problem(nv, np.random.default_rng(21), 128, 16, 4, 2, new, lens, 0.07)
+    args = (ints(table), ints(cumulative(new)), ints(lens))
+    for causal in (True, False):
+        want, lse0 = nv.paged_attention(q, cache, *args, causal=causal, max_q=max_q, want_lse=True)
+        for window in (1 << 20, (1 << 31) - 1, 1 << 31, (1 << 63) - (1 << 31), (1 << 63) - 1):
+            out, lse = nv.paged_attention(q, cache, *args, causal=causal, window=window, max_q=max_q, want_lse=True)
+            assert torch.equal(out, want) and torch.equal(lse, lse0), window
+    assert nv.device_status() == 0
