@@ -338,7 +338,8 @@ nvfp4_status nvfp4_quantize_noalloc(const void* x, int64_t M, int64_t K, nvfp4_m
  *              128.
  * k_g, v_g     device FP32 scalars: static global scales of K and V (finite, not
  *              negative).
- * block_table  [batch][table_width] int32: page j of sequence b.
+ * block_table  [batch][table_width] int32: page j of sequence b;
+ *              table_width * page_size at most 2^31 - 256.
  * cu_q         [batch + 1] int32, non-decreasing: rows [cu_q[b], cu_q[b+1]) of
  *              the new-token tensors belong to sequence b.
  * kv_len       [batch] int32: cached tokens of b, the new ones included. New

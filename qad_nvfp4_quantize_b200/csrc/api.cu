@@ -59,9 +59,11 @@ bool kv_shape_ok(int page_size, int head_dim) {
   return (page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128) &&
          (head_dim == 64 || head_dim == 128);
 }
+// Token indexes are 32-bit numbers, up to two tiles of 128 behind a sequence's last token.
+constexpr int64_t kMostKvTokens = (int64_t(1) << 31) - 256;
 bool kv_sizes_ok(int64_t total, int kv_heads, int batch, int table_width, int64_t num_pages, int page_size) {
   return total >= 0 && total < (int64_t(1) << 31) && kv_heads > 0 && kv_heads <= 1024 && batch >= 0 &&
-         batch < (1 << 24) && table_width >= 0 && (int64_t)table_width * page_size < (int64_t(1) << 31) &&
+         batch < (1 << 24) && table_width >= 0 && (int64_t)table_width * page_size <= kMostKvTokens &&
          num_pages >= 0 && num_pages < (int64_t(1) << 31);
 }
 bool pool_ok(int64_t num_pages, int slots, int table_width, int page_size) {

@@ -1,0 +1,17 @@
+"""CPU-only checks of the paged KV cache's borders: what the C entry points refuse before any launch."""
+import pytest
+
+import qad_nvfp4_quantize_b200 as nv
+from tests.test_kv_cache_host import APPEND, ATTN
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_tables_of_nearly_2_31_tokens(page):
+    # token indexes, up to two tiles of 128 behind the last one, are 32-bit numbers
+    most = (1 << 31) // page - 256 // page
+    L = nv.lib()
+    for width, status in ((most, 4), (most + 1, 1), ((1 << 31) // page - 1, 1), ((1 << 31) // page, 1)):
+        # (without a workspace: what is not refused for its sizes ends there)
+        assert L.nvfp4_paged_attention(*dict(ATTN, page=page, width=width, ws=None).values(), None) == status
+    for width in (most + 1, (1 << 31) // page - 1):
+        assert L.nvfp4_kv_append(*dict(APPEND, page=page, width=width).values(), None) == 1
