@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          top[nt][c] = max2(max3(s[nt][0][c], s[nt][0][c + 2], s[nt][1][c]), s[nt][1][c + 2]) * factor[nt][c];
-          grow |= takes_new_max(top[nt][c], m[nt][c]);
+          top[nt][c] = fmaxf(max3(s[nt][0][c], s[nt][0][c + 2], s[nt][1][c]), s[nt][1][c + 2]) * factor[nt][c];
+          grow |= exceeds(top[nt][c], m[nt][c]);
         }
       if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
@@ -349,9 +349,9 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float mx = top[nt][c];
-            mx = max2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-            mx = max2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-            mx = max2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
             const float m1 = new_max(mx, m[nt][c]);
             const float f = m[nt][c] == kStartMax ? 0.0f : ex2(m[nt][c] - m1);
             m[nt][c] = m1;
@@ -424,7 +424,8 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       __syncwarp();  // the stage may be refilled
     }
 
-    // ---- the warps' parts meet
+    // ---- the warps' parts meet. (A row with a score of NaN or +Inf, from a query that holds NaN or Inf, shows it in its
+    // sum l alone: l is multiplied by 0, never left out, where a part saw nothing.)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
         const int row = 8 * nt + 2 * t + c;
         float mt = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) mt = max2(mt, sh.wm[w][row]);
+        for (int w = 0; w < kAttnWarps; ++w) mt = fmaxf(mt, sh.wm[w][row]);
         const float f = m[nt][c] == -INFINITY ? 0.0f : ex2(m[nt][c] - mt);
 #pragma unroll
         for (int j = 0; j < kSteps; ++j)  // dimensions 2j, 2j+1 of the run of D/8 that starts at g*D/8
@@ -460,9 +461,9 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       }
     if (tid < kRows) {
       float mt = -INFINITY, lt = 0.0f;
-      for (int w = 0; w < kAttnWarps; ++w) mt = max2(mt, sh.wm[w][tid]);
+      for (int w = 0; w < kAttnWarps; ++w) mt = fmaxf(mt, sh.wm[w][tid]);
       for (int w = 0; w < kAttnWarps; ++w)
-        lt += sh.wm[w][tid] == -INFINITY ? 0.0f : sh.wl[w][tid] * ex2(sh.wm[w][tid] - mt);
+        lt += sh.wl[w][tid] * (sh.wm[w][tid] == -INFINITY ? 0.0f : ex2(sh.wm[w][tid] - mt));
       sh.m[tid] = mt;
       sh.l[tid] = lt;
     }
@@ -551,12 +552,11 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
                 y[c].l = __ldcg(from + kRows * D + kRows + row);
               }
             }
-            float mt = x.m;
+            float mt = fmaxf(x.m, kStartMax);  // finite also where no token has been seen so far
 #pragma unroll
-            for (int c = 0; c < kBatch; ++c) mt = max2(mt, y[c].m);
-            if (mt == -INFINITY) continue;  // no visible token so far
+            for (int c = 0; c < kBatch; ++c) mt = fmaxf(mt, y[c].m);
             auto add = [&](Sums& to, const Sums& z) {
-              const float f = ex2(z.m - mt);  // 0 for a part without a visible token: its sums are zeros
+              const float f = ex2(z.m - mt);  // 0 for a part without a visible token: its sums are zeros, or l is NaN
               to.o.x += z.o.x * f;
               to.o.y += z.o.y * f;
               to.o.z += z.o.z * f;

@@ -47,15 +47,18 @@ NVFP4_DEVINL float ex2(float x) {
   return r;
 }
 
-// Maxima that are NaN if an argument is. A visible score that is NaN (a query
-// that holds NaN or Inf) then makes its row's maximum NaN, and with it all that
-// is scaled by it, whichever parts the row's tokens are divided into.
-NVFP4_DEVINL float max2(float a, float b) {
+NVFP4_DEVINL float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Maxima that are NaN if an argument is.
+NVFP4_DEVINL float max2_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-NVFP4_DEVINL float max3(float a, float b, float c) {
+NVFP4_DEVINL float max3_nan(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
@@ -141,14 +144,10 @@ constexpr float kRescaleAt = 8.0f, kHeadroom = 7.0f;
 constexpr float kStartMax = -1e30f;                // running maximum before the first visible token
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
-// A row whose largest new score is `top` keeps its running maximum m (so that
-// its neighbours do not change its result) or takes a new one: where top exceeds
-// m by more than head-room and lag, or either is NaN. A score of +Inf has no softmax: NaN too.
-NVFP4_DEVINL bool takes_new_max(float top, float m) { return !(top <= m + (kRescaleAt + kHeadroom)); }
-NVFP4_DEVINL float new_max(float top, float m) {
-  if (!takes_new_max(top, m)) return m;
-  return top == INFINITY ? NAN : max2(top - kHeadroom, m);
-}
+// A row whose largest new score is `top` keeps its running maximum m, whatever
+// its neighbours do, or takes a new one where top exceeds m by more.
+NVFP4_DEVINL bool exceeds(float top, float m) { return top > m + (kRescaleAt + kHeadroom); }
+NVFP4_DEVINL float new_max(float top, float m) { return exceeds(top, m) ? top - kHeadroom : m; }
 
 // The same value in every lane, in a form that the compiler knows to be uniform.
 NVFP4_DEVINL int uniform(int v) { return __reduce_max_sync(0xFFFFFFFFu, v); }

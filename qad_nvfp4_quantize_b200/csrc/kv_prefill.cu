@@ -401,14 +401,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
 #pragma unroll
           for (int e = 0; e < 64; e += 8) {
-            t0 = max3(t0, __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
-            t1 = max3(t1, __uint_as_float(y[e + 2]), __uint_as_float(y[e + 3]));
-            t2 = max3(t2, __uint_as_float(y[e + 4]), __uint_as_float(y[e + 5]));
-            t3 = max3(t3, __uint_as_float(y[e + 6]), __uint_as_float(y[e + 7]));
+            t0 = max3_nan(t0, __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+            t1 = max3_nan(t1, __uint_as_float(y[e + 2]), __uint_as_float(y[e + 3]));
+            t2 = max3_nan(t2, __uint_as_float(y[e + 4]), __uint_as_float(y[e + 5]));
+            t3 = max3_nan(t3, __uint_as_float(y[e + 6]), __uint_as_float(y[e + 7]));
           }
-          const float top = max3(max2(t0, t1), t2, t3) * factor;
-          if (__any_sync(0xFFFFFFFFu, takes_new_max(top, m))) {
-            const float m1 = new_max(top, m);
+          const float top = max3_nan(max2_nan(t0, t1), t2, t3) * factor;
+          if (__any_sync(0xFFFFFFFFu, !(top <= m + (kRescaleAt + kHeadroom)))) {
+            // (a score of NaN or +Inf stays in m: the sum would not show it where exp2_poly has its place)
+            const float m1 = top < INFINITY ? new_max(top, m) : NAN;
             const float f = m == kStartMax ? 0.0f : ex2(m - m1);
             m = m1;
             l *= f;
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           if (!(ok = meet())) break;
           if (sh.last[i]) {
             float mt = -INFINITY, lt = 0.0f;
-            for (int64_t c = c0; c <= c1; ++c) mt = max2(mt, __ldcg(part_of(c, c == c0) + row));
+            for (int64_t c = c0; c <= c1; ++c) mt = max2_nan(mt, __ldcg(part_of(c, c == c0) + row));
             for (int64_t c = c0; c <= c1; ++c) {
               const float mc = __ldcg(part_of(c, c == c0) + row);
               lt += mc == -INFINITY ? 0.0f : __ldcg(part_of(c, c == c0) + 128 + row) * ex2(mc - mt);
