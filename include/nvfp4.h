@@ -488,6 +488,23 @@ nvfp4_status nvfp4_selftest_gemm_timeout(const uint8_t* Aq, const uint8_t* As, c
                                          int64_t M, int64_t N, int64_t K, void* C, uint64_t timeout_ns,
                                          nvfp4_stream_t stream);
 
+/* Test hook for the paged attention's bounded waits: nvfp4_paged_attention with
+ * the same arguments, except that the first copies of cached tokens are awaited
+ * but not issued and every wait gives up after about `timeout_ns` (0 <
+ * timeout_ns <= 10 s). Where there are cached tokens the waits run out: the call
+ * records NVFP4_ERR_TIMEOUT in the device status word, lets its issued copies
+ * and MMAs finish (bounded), frees its tensor memory and returns; out and lse
+ * are then unspecified, the workspace has to be zero-filled again, and the
+ * context stays usable. */
+nvfp4_status nvfp4_selftest_attention_timeout(const void* q, int64_t q_stride, int64_t total, int q_heads,
+                                              int kv_heads, int head_dim, const int32_t* cu_q,
+                                              const int32_t* kv_len, int batch, const int32_t* block_table,
+                                              int table_width, const uint8_t* pages, int64_t num_pages,
+                                              int page_size, const float* k_g, const float* v_g, float scale,
+                                              int causal, int64_t window, int64_t max_q, void* out, float* lse,
+                                              void* workspace, size_t workspace_bytes, uint64_t timeout_ns,
+                                              nvfp4_stream_t stream);
+
 /* FP4 tensor-core rate probe (diagnostic; the pages have no counterpart):
  * launches one CTA per SM that issues `iters` x 4 block-scaled MMAs
  * (kind::mxf4nvf4, M=128, N=256, K=64 -- the W4A4 GEMM's instruction) on

@@ -20,7 +20,7 @@ __all__ = [
     "check_device", "scale_bytes", "quantize", "fake_quant", "fake_quant_backward", "dequantize", "topk_kl", "gemm", "moe_grouped_gemm",
     "moe_workspace_layout", "convert_e2m1", "convert_e4m3", "device_status", "selftest_timeout",
     "quantize_workspace_bytes", "moe_workspace_bytes", "quantize_experts", "quantize_noalloc",
-    "selftest_gemm_timeout", "kernel_launches", "probe_mma_peak",
+    "selftest_gemm_timeout", "selftest_attention_timeout", "kernel_launches", "probe_mma_peak",
     "KVCache", "kv_cache", "kv_page_bytes", "kv_append", "paged_attention", "kv_copy_pages", "kv_fork", "kv_free",
     "kv_compact",
 ]
@@ -94,6 +94,8 @@ _SIGS = {
     "nvfp4_get_device_status": (I32, [P, I32, ctypes.POINTER(ctypes.c_int)]),
     "nvfp4_selftest_timeout": (I32, [U64, P]),
     "nvfp4_selftest_gemm_timeout": (I32, [P, P, P, P, P, P, I64, I64, I64, P, U64, P]),
+    "nvfp4_selftest_attention_timeout": (I32, [P, I64, I64, I32, I32, I32, P, P, I32, P, I32, P, I64, I32, P, P, F32,
+                                               I32, I64, I64, P, P, P, SZ, U64, P]),
     "nvfp4_kernel_launches": (U64, []),
     "nvfp4_probe_mma_peak": (I32, [I32, ctypes.POINTER(ctypes.c_double), P]),
 }
@@ -673,6 +675,24 @@ def selftest_gemm_timeout(a: Quantized, b: Quantized, timeout_ns: int, out: Opti
                                              _ptr(b.scales), _ptr(b.g), a.rows, b.rows, a.K, _ptr(C), timeout_ns,
                                              _stream(dev)), "nvfp4_selftest_gemm_timeout")
     return C
+
+
+def selftest_attention_timeout(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
+                               kv_len: torch.Tensor, timeout_ns: int, max_q: int = 0) -> None:
+    """nvfp4_selftest_attention_timeout: the paged attention with its first
+    copies left unissued, so that its bounded waits run out (device status 6).
+    On a workspace of its own; the result is dropped."""
+    index, num_pages, heads, _ = _kv_cache_of(cache)
+    dim, batch, width = cache.head_dim, kv_len.shape[0], block_table.shape[-1]
+    stride = _rows(q, "q", index, None, dim)
+    total, hq, _ = q.shape
+    out = q.new_empty((total, hq, dim))
+    ws = torch.zeros(int(lib().nvfp4_paged_attention_workspace_bytes()), dtype=torch.uint8, device=q.device)
+    _call("nvfp4_selftest_attention_timeout", index, q.data_ptr(), stride, total, hq, heads, dim,
+          _ints(cu_q, "cu_q", index, batch + 1), _ints(kv_len, "kv_len", index, batch), batch,
+          _ints(block_table, "block_table", index, batch, width), width, cache.pages.data_ptr(), num_pages,
+          cache.page_size, cache.k_g.data_ptr(), cache.v_g.data_ptr(), dim ** -0.5, 1, 0, max_q, out.data_ptr(), None,
+          ws.data_ptr(), ws.numel(), timeout_ns)
 
 
 def selftest_timeout(timeout_ns: int, device=None) -> None:

@@ -323,12 +323,12 @@ nvfp4_status nvfp4_kv_append(const void* k, const void* v, int64_t row_stride, i
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
-nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_stride, int64_t total, int q_heads, int kv_heads,
-                                   int head_dim, const int32_t* cu_q, const int32_t* kv_len, int batch,
-                                   const int32_t* block_table, int table_width, const uint8_t* pages,
-                                   int64_t num_pages, int page_size, const float* k_g, const float* v_g, float scale,
-                                   int causal, int64_t window, int64_t max_q, void* out, float* lse, void* workspace,
-                                   size_t workspace_bytes, nvfp4_stream_t stream) {
+static nvfp4_status run_attention(const void* q, int64_t q_stride, int64_t total, int q_heads, int kv_heads,
+                                  int head_dim, const int32_t* cu_q, const int32_t* kv_len, int batch,
+                                  const int32_t* block_table, int table_width, const uint8_t* pages,
+                                  int64_t num_pages, int page_size, const float* k_g, const float* v_g, float scale,
+                                  int causal, int64_t window, int64_t max_q, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, nvfp4_stream_t stream, int64_t wait_cycles, int withheld) {
   if (!kv_shape_ok(page_size, head_dim) || !kv_sizes_ok(total, kv_heads, batch, table_width, num_pages, page_size))
     return NVFP4_ERR_INVALID_ARG;
   if (q_heads <= 0 || q_heads % kv_heads || q_heads / kv_heads > 128) return NVFP4_ERR_INVALID_ARG;
@@ -361,8 +361,34 @@ nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_stride, int64_t tota
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = d->status;
+  a.wait_cycles = wait_cycles;
+  a.withheld = withheld;
   return launched(nvfp4::launch_kv_attention(a, head_dim, max_q, workspace, d->num_sms,
                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_stride, int64_t total, int q_heads, int kv_heads,
+                                   int head_dim, const int32_t* cu_q, const int32_t* kv_len, int batch,
+                                   const int32_t* block_table, int table_width, const uint8_t* pages,
+                                   int64_t num_pages, int page_size, const float* k_g, const float* v_g, float scale,
+                                   int causal, int64_t window, int64_t max_q, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, nvfp4_stream_t stream) {
+  return run_attention(q, q_stride, total, q_heads, kv_heads, head_dim, cu_q, kv_len, batch, block_table, table_width,
+                       pages, num_pages, page_size, k_g, v_g, scale, causal, window, max_q, out, lse, workspace,
+                       workspace_bytes, stream, nvfp4::kAttnWaitCycles, 0);
+}
+
+nvfp4_status nvfp4_selftest_attention_timeout(const void* q, int64_t q_stride, int64_t total, int q_heads,
+                                              int kv_heads, int head_dim, const int32_t* cu_q, const int32_t* kv_len,
+                                              int batch, const int32_t* block_table, int table_width,
+                                              const uint8_t* pages, int64_t num_pages, int page_size,
+                                              const float* k_g, const float* v_g, float scale, int causal,
+                                              int64_t window, int64_t max_q, void* out, float* lse, void* workspace,
+                                              size_t workspace_bytes, uint64_t timeout_ns, nvfp4_stream_t stream) {
+  if (timeout_ns == 0 || timeout_ns > 10000000000ull) return NVFP4_ERR_INVALID_ARG;  // (0, 10 s]
+  return run_attention(q, q_stride, total, q_heads, kv_heads, head_dim, cu_q, kv_len, batch, block_table, table_width,
+                       pages, num_pages, page_size, k_g, v_g, scale, causal, window, max_q, out, lse, workspace,
+                       workspace_bytes, stream, 2 * (int64_t)timeout_ns, 1);  // at about 2 cycles a nanosecond
 }
 
 nvfp4_status nvfp4_kv_copy_pages(uint8_t* pages, int64_t num_pages, int64_t page_bytes, const int32_t* src,

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
   fence_proxy_async_smem();
   __syncthreads();  // the search's scratch lies over the ring
   uint32_t phase = 0;  // parity bit of each stage of this warp's ring
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity, &sh.abort); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity, &sh.abort, a.wait_cycles); };
   const float kg = *a.k_g, vg = *a.v_g;
 
   for (int64_t u = u0;;) {
@@ -190,18 +190,18 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       }
       there_next = __ballot_sync(0xFFFFFFFFu, good);
     };
-    auto issue = [&](int i, int st) {  // called by the whole warp, i in order
+    auto issue = [&](int i, int st, bool withheld) {  // called by the whole warp, i in order
       if ((i & 15) == 0) look_up(i);
       const uint32_t two = (there_next >> (2 * (i & 15))) & 3u;
       if (two == 0) return;
       if (lane == 0) mbar_arrive_expect_tx(&sh.bar[warp][st], (uint32_t)__popc(two) * kGB);
       __syncwarp();
-      if ((lane >> 1) == (i & 15) && ((there_next >> lane) & 1u))
+      if (!withheld && (lane >> 1) == (i & 15) && ((there_next >> lane) & 1u))
         bulk_load(sh.ring[warp][st] + (lane & 1) * kGB, from, kGB, &sh.bar[warp][st]);
     };
     int ahead = 0, st_ahead = 0, st = 0;
     for (; ahead < cnt && ahead < kStages - 1; ++ahead) {
-      issue(ahead, st_ahead++);
+      issue(ahead, st_ahead++, ahead < a.withheld);
       if ((ahead & 15) == 0) there = there_next;
     }
 
@@ -253,15 +253,16 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
     }
 
+    bool ok = true;
     for (int i = 0; i < cnt; ++i) {
       if ((i & 15) == 0) there = there_next;  // the look-up of this block ran at most kStages - 1 pairs ago
       const uint32_t two = (there >> (2 * (i & 15))) & 3u;
       if (ahead < cnt) {  // into the stage that the last trip has read
-        issue(ahead++, st_ahead);
+        issue(ahead++, st_ahead, false);
         if (++st_ahead == kStages) st_ahead = 0;
       }
       if (two) {
-        if (!wait(&sh.bar[warp][st], (phase >> st) & 1u) && lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
+        if (!(ok = wait(&sh.bar[warp][st], (phase >> st) & 1u))) break;
         phase ^= 1u << st;
       }
       const uint8_t* gr = sh.ring[warp][st];
@@ -424,6 +425,11 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       __syncwarp();  // the stage may be refilled
     }
 
+    if (!ok) {
+      if (lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
+      for (int x = 0; x < kStages; ++x) settle(&sh.bar[warp][x], (phase >> x) & 1u);
+    }
+
     // ---- the warps' parts meet. (A row with a score of NaN or +Inf, from a query that holds NaN or Inf, shows it in its
     // sum l alone: l is multiplied by 0, never left out, where a part saw nothing.)
 #pragma unroll
@@ -445,6 +451,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
         }
       }
     __syncthreads();  // every warp has read its ring: the joining buffer may take its place
+    if (sh.abort) return;  // (set before this barrier only: the next wait lies behind others)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -122,8 +122,9 @@ struct AttnArgs {
   float* partial;      // workspace
   int32_t* counters;   // workspace, zero between calls
   int* status;
+  int64_t wait_cycles;  // bound of every wait
+  int withheld;         // 1 in the self-test: the first copies are awaited but not issued
 };
-
 
 // One thread's arrival, after a barrier of its CTA, at a counter of CTAs that
 // have stored their parts: true for the last of `others` + 1, which may then
@@ -135,7 +136,7 @@ NVFP4_DEVINL int arrive_last(int32_t* counter, int others) {
   return before == others;
 }
 
-constexpr int64_t kAttnWaitCycles = 4000000000ll;  // bound of every wait, about 2 s
+constexpr int64_t kAttnWaitCycles = 4000000000ll;  // about 2 s
 // The running maximum m of a row is held kHeadroom below the score that set it (in log2 units) and may lag kRescaleAt
 // behind a larger one, so a row's largest weight 2^(s - m) lies in [2^7, 2^15]: weights are FP16 operands, which hold
 // 11 bits down to 2^-14 and multiples of 2^-24 below. Without the head-room tokens 16 nats below an attention sink lost
@@ -153,20 +154,28 @@ NVFP4_DEVINL float new_max(float top, float m) { return exceeds(top, m) ? top - 
 NVFP4_DEVINL int uniform(int v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
 
 // Wait of a whole warp for a phase of an mbarrier, given up (false) after
-// kAttnWaitCycles or when another warp gave up. Every lane polls: one lane
+// `cycles` or when another warp gave up. Every lane polls: one lane
 // polling for the others measured 580 cycles from arrival to return with 16
 // warps waiting, this 130.
-NVFP4_DEVINL bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort) {
+NVFP4_DEVINL bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort, int64_t cycles) {
   if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
   uint32_t spins = 0;
   const int64_t t0 = clock64();
   while (true) {
     const bool done = mbar_try_wait(bar, parity);
     if (__all_sync(0xFFFFFFFFu, done)) return true;
-    if ((++spins & 15u) == 0 && __any_sync(0xFFFFFFFFu, *abort || clock64() - t0 > kAttnWaitCycles)) {
+    if ((++spins & 15u) == 0 && __any_sync(0xFFFFFFFFu, *abort || clock64() - t0 > cycles)) {
       *abort = 1;
       return false;
     }
+  }
+}
+
+// A warp that gave up lets what may be in flight (copies, MMAs) arrive, 1 ms at
+// most: it must not land in a CTA that gets the same memory later.
+NVFP4_DEVINL void settle(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < 1000000ull) {
   }
 }
 

@@ -67,7 +67,7 @@ struct PreShared {
   uint64_t codes_full[kStages], codes_empty[kStages];
   uint32_t there[kStages];  // bit g: granule g of the tile is there (within the span, on a page of the pool)
   uint64_t full[kTiles], empty[kTiles];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], group[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], group[2], drain[2];
   Part<kPreRows> part;
   WorkCursor<kPreRows> cursor[kPreThreads / 32];  // one per warp: no register is spent on it
   uint32_t tmem;
@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       mbar_init(&sh.pv_done[i][0], 1);
       mbar_init(&sh.pv_done[i][1], 1);
       mbar_init(&sh.group[i], 4);
+      mbar_init(&sh.drain[i], 1);
     }
     sh.abort = 0;
     fence_barrier_init();
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   auto timed_out = [&]() {
     if (lane == 0) record_status(a.status, NVFP4_ERR_TIMEOUT);
   };
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity, &sh.abort); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded(bar, parity, &sh.abort, a.wait_cycles); };
   // place of K (2t) or V (2t + 1) in the ring of tiles, and the parity of its turn there
   auto place = [](uint32_t x) { return x % Sh::kTiles; };
   auto turn_of = [](uint32_t x) { return (x / Sh::kTiles) & 1; };
@@ -639,17 +640,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           mbar_arrive_expect_tx(&sh.codes_full[st], (uint32_t)__popc(there) * kGB);
         }
         __syncwarp();
-        if (lane < 8 && good) bulk_load(sh.codes[st][lane], head + at, kGB, &sh.codes_full[st]);
+        if (lane < 8 && good && it >= (uint32_t)a.withheld) bulk_load(sh.codes[st][lane], head + at, kGB, &sh.codes_full[st]);
         page = next;
       }
       if (!ok || !next_work()) break;
     }
-    if (!ok) {
-      timed_out();
-      const uint64_t t0 = globaltimer_ns();  // copies in flight land before the CTA may exit
-      while (globaltimer_ns() - t0 < 1000000ull) {
-      }
-    }
+    if (!ok) timed_out();
+    // the last tiles' copies land, even if those who wait for them gave up
+    for (uint32_t x = it < kStages ? 0 : it - kStages; x < it; ++x) settle(&sh.codes_full[x % kStages], (x / kStages) & 1);
+    __syncwarp();
   } else {
     // ----------------------------------------------------------- MMA issue
     if (warp < 14) {
@@ -708,11 +707,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       }
       if (!ok) {
         timed_out();
-        if (lane == 0) {  // MMAs in flight read shared memory: a grace time, then the CTA may exit
-          const uint64_t t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < 1000000ull) {
-          }
-        }
+        tc_commit_elect(&sh.drain[i]);  // MMAs in flight read shared memory
+        settle(&sh.drain[i], 0);
       }
       __syncwarp();
     }

@@ -186,3 +186,33 @@ def test_a_window_of_any_size(nv, max_q):
             out, lse = nv.paged_attention(q, cache, *args, causal=causal, window=window, max_q=max_q, want_lse=True)
             assert torch.equal(out, want) and torch.equal(lse, lse0), window
     assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("max_q", [1, 4, 64])
+def test_attention_waits_that_run_out(nv, max_q, D):
+    """Copies that are awaited but never issued: the waits give up and are reported, what is in flight lands before the
+    blocks leave, calls beside it and behind it are right."""
+    new, lens = [2, 1], [30000, 700]
+    q, _, cache, _, table = problem(nv, np.random.default_rng(22), D, 32, 8, 2, new, lens, 0.07)
+    args = (ints(table), ints(cumulative(new)), ints(lens))
+    want, lse0 = nv.paged_attention(q, cache, *args, max_q=max_q, want_lse=True)
+    assert nv.device_status() == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            nv.selftest_attention_timeout(q, cache, *args, timeout_ns=1_000_000, max_q=max_q)
+        beside = [nv.paged_attention(q, cache, *args, max_q=max_q, want_lse=True) for _ in range(20)]
+        torch.cuda.synchronize()
+        assert nv.device_status() == 6
+        out, lse = nv.paged_attention(q, cache, *args, max_q=max_q, want_lse=True)
+        for x, y in beside + [(out, lse)]:
+            assert torch.equal(x, want) and torch.equal(y, lse0)
+        assert nv.device_status() == 0
+    # nothing cached: nothing is awaited
+    nv.selftest_attention_timeout(q, cache, args[0], args[1], ints([0, 0]), timeout_ns=1_000_000, max_q=max_q)
+    torch.cuda.synchronize()
+    assert nv.device_status() == 0
+    with pytest.raises(nv.NVFP4Error):
+        nv.selftest_attention_timeout(q, cache, *args, timeout_ns=0)

@@ -15,3 +15,9 @@ def test_tables_of_nearly_2_31_tokens(page):
         assert L.nvfp4_paged_attention(*dict(ATTN, page=page, width=width, ws=None).values(), None) == status
     for width in (most + 1, (1 << 31) // page - 1):
         assert L.nvfp4_kv_append(*dict(APPEND, page=page, width=width).values(), None) == 1
+
+
+def test_attention_timeout_self_test_refuses_its_limits():
+    # (no limit, more than 10 s; a workspace that is missing ends what is not refused for its limit)
+    for limit, status in ((0, 1), (10_000_000_001, 1), (1_000_000, 4)):
+        assert nv.lib().nvfp4_selftest_attention_timeout(*dict(ATTN, ws=None).values(), limit, None) == status
