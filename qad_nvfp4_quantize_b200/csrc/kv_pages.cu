@@ -69,10 +69,14 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(uint4* pages, int
     uint4 r[kCopyLoads];
 #pragma unroll
     for (int e = 0; e < kCopyLoads; ++e)
-      if (at + e * kCopyThreads < page_vecs) r[e] = ld_stream(from + at + e * kCopyThreads);
+      if (at + e * kCopyThreads < page_vecs &&
+          NVFP4_IN_BOUNDS(a * page_vecs + at + e * kCopyThreads, num_pages * page_vecs, status))
+        r[e] = ld_stream(from + at + e * kCopyThreads);
 #pragma unroll
     for (int e = 0; e < kCopyLoads; ++e)
-      if (at + e * kCopyThreads < page_vecs) to[at + e * kCopyThreads] = r[e];
+      if (at + e * kCopyThreads < page_vecs &&
+          NVFP4_IN_BOUNDS(b * page_vecs + at + e * kCopyThreads, num_pages * page_vecs, status))
+        to[at + e * kCopyThreads] = r[e];
   }
 }
 
@@ -107,7 +111,11 @@ NVFP4_DEVINL int32_t slot_len(const PoolIndex& p, int32_t slot, int* status) {
 // Entry j of child i's row of the table: a shared page counted once more, or the
 // part page's copy.
 NVFP4_DEVINL void fork_entry(const PoolIndex& p, int a, int c, int to, int64_t j, int* status) {
-  const int64_t full = p.seq_len[c] / p.page;
+  const int64_t full = p.seq_len[c] / p.page, entries = (int64_t)p.slots * p.width;
+  if (j > full || (j == full && to < 0)) return;
+  if (!NVFP4_IN_BOUNDS(j, p.width, status) || !NVFP4_IN_BOUNDS((int64_t)a * p.width + j, entries, status) ||
+      !NVFP4_IN_BOUNDS((int64_t)c * p.width + j, entries, status))
+    return;
   if (j < full) {
     const int64_t page = p.table[(int64_t)a * p.width + j];
     p.table[(int64_t)c * p.width + j] = (int32_t)page;
@@ -115,7 +123,7 @@ NVFP4_DEVINL void fork_entry(const PoolIndex& p, int a, int c, int to, int64_t j
       record_status(status, NVFP4_ERR_PAGE);
     else
       atomicAdd(&p.refs[page], 1);
-  } else if (j == full && to >= 0) {
+  } else {
     p.table[(int64_t)c * p.width + j] = to;
   }
 }
@@ -186,7 +194,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(PoolIndex p,
     int sum;
     int r = found + block_exclusive_scan(__popc(mask), sh, &sum);
     found += sum;
-    for (; mask && r < need; mask &= mask - 1, ++r) dst[r] = (int32_t)(at + __ffs(mask) - 1);
+    for (; mask && r < need; mask &= mask - 1, ++r)
+      if (NVFP4_IN_BOUNDS(r, n, status) && NVFP4_IN_BOUNDS(at + __ffs(mask) - 1, p.num_pages, status))
+        dst[r] = (int32_t)(at + __ffs(mask) - 1);
   }
   __syncthreads();
   if (found < need) {  // too few: the pool stays as it was
@@ -202,14 +212,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(PoolIndex p,
   for (int i0 = (n - 1) / kPlanThreads * kPlanThreads; i0 >= 0; i0 -= kPlanThreads) {
     const int i = i0 + t;
     const int r = i < n ? src[i] : -2;
-    const int page = r >= 0 ? dst[r] : r;
+    const int page = r >= 0 && NVFP4_IN_BOUNDS(r, n, status) ? dst[r] : r;
     __syncthreads();
     if (i < n) {
       dst[i] = page;
       if (r >= 0) {
         const int a = parent[i];
-        const int64_t part = p.table[(int64_t)a * p.width + p.seq_len[child[i]] / p.page];
-        p.refs[page] = 1;
+        const int64_t from = (int64_t)a * p.width + p.seq_len[child[i]] / p.page;
+        const int64_t part = NVFP4_IN_BOUNDS(from, (int64_t)p.slots * p.width, status) ? p.table[from] : -1;
+        if (NVFP4_IN_BOUNDS(page, p.num_pages, status)) p.refs[page] = 1;
         if (part < 0 || part >= p.num_pages) record_status(status, NVFP4_ERR_PAGE);
         src[i] = part < 0 || part >= p.num_pages ? -1 : (int32_t)part;  // nothing to copy from
       }
@@ -271,6 +282,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_free_kernel(PoolIndex p, const
   }
   __syncthreads();
   for (int64_t j = threadIdx.x; j < held; j += kRowThreads) {
+    if (!NVFP4_IN_BOUNDS((int64_t)slot * p.width + j, (int64_t)p.slots * p.width, status)) continue;
     int32_t* at = p.table + (int64_t)slot * p.width + j;
     const int64_t page = *at;
     *at = -1;
@@ -322,7 +334,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_count_kernel(const in
 __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const int32_t* refs, int64_t n,
                                                                        const int32_t* counted, int chunks,
                                                                        int32_t* refs_out, int32_t* src, int32_t* dst,
-                                                                       int64_t cap, int32_t* rank_of, int32_t* live) {
+                                                                       int64_t cap, int32_t* rank_of, int32_t* live,
+                                                                       int* status) {
   __shared__ int sh[kPlanWarps + 1];
   __shared__ int32_t small[kSmallChunks];
   const int t = threadIdx.x;
@@ -378,9 +391,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const int
     const bool u = (used >> e) & 1u;
     if (p < L) {
       if (u) refs_out[p] = refs[p];
-      else dst[p - rank] = (int32_t)p;  // its count comes with the page that moves here
+      else if (NVFP4_IN_BOUNDS(p - rank, cap, status)) dst[p - rank] = (int32_t)p;  // (its count comes with its new page)
     } else if (u) {
-      src[rank - below] = (int32_t)p;
+      if (NVFP4_IN_BOUNDS(rank - below, cap, status)) src[rank - below] = (int32_t)p;
       rank_of[p] = rank - below;
     } else {
       refs_out[p] = 0;
@@ -405,8 +418,10 @@ __global__ void __launch_bounds__(kRowThreads) kv_compact_apply_kernel(PoolIndex
     for (int64_t r = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; r < cap; r += (int64_t)ref_blocks * kRowThreads) {
       const int32_t a = src[r];
       if (a < 0) return;  // the moves come first
+      const int32_t b = dst[r];
+      if (!NVFP4_IN_BOUNDS(a, p.num_pages, status) || !NVFP4_IN_BOUNDS(b, p.num_pages, status)) continue;
       const int32_t count = p.refs[a];
-      refs_out[dst[r]] = count;
+      refs_out[b] = count;
       refs_out[a] = 0;
     }
     return;
@@ -420,9 +435,10 @@ __global__ void __launch_bounds__(kRowThreads) kv_compact_apply_kernel(PoolIndex
     if (j < held) {
       if (page < 0 || page >= p.num_pages || (page >= L && rank_of[page] < 0))
         record_status(status, NVFP4_ERR_PAGE);  // not a page of this pool, or one that nobody holds
-      else if (page >= L)
+      else if (page >= L && NVFP4_IN_BOUNDS(rank_of[page], cap, status))
         page = dst[rank_of[page]];
     }
+    if (!NVFP4_IN_BOUNDS(row * p.width + j, (int64_t)p.slots * p.width, status)) continue;
     table_out[row * p.width + j] = (int32_t)page;
   }
 }
@@ -448,7 +464,7 @@ cudaError_t launch_kv_compact(const PoolArgs& a, int32_t* refs_out, int32_t* tab
   }
   note_launch();
   kv_compact_plan_kernel<<<chunks, kPlanThreads, 0, s>>>(a.refs, n, chunks > kSmallChunks ? counts : nullptr, chunks,
-                                                        refs_out, src, dst, cap, rank_of, live);
+                                                        refs_out, src, dst, cap, rank_of, live, status);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   note_launch();

@@ -370,7 +370,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         const int32_t* table = a.ix.table + (int64_t)w.b * a.ix.width;
         const int32_t gend = w.span.g0 + w.span.n;
         int32_t gi = w.span.g0 + kUnitGranules * j0 + (lane & 3);
-        int32_t page = gi < gend ? table[gi >> a.ix.gshift] : 0;
+        auto page_at = [&](int32_t g) {
+          return g < gend && NVFP4_IN_BOUNDS(g >> a.ix.gshift, a.ix.width, a.status) ? table[g >> a.ix.gshift] : 0;
+        };
+        int32_t page = page_at(gi);
         int32_t tok0 = (w.span.g0 + kUnitGranules * j0) * kGranule;
         const int32_t all_lo = last_row.lo, all_hi = w.span.n > 0 ? first_row.hi : 0;
 
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         for (int x = 2 * (j1 - j0); x > 0; --x, ++steps, tok0 += 64) {
           const uint32_t bad = __ballot_sync(0xFFFFFFFFu, page < 0 || page >= a.ix.num_pages);
           gi += 4;
-          page = gi < gend ? table[gi >> a.ix.gshift] : 0;
+          page = page_at(gi);
           const bool whole = tok0 >= all_lo && tok0 + 64 <= all_hi && bad == 0;
           const uint32_t t_x = t_s + 64 * (steps & 1);
           if (!(ok = wait(&sh.s_full[i][steps & 1], (steps >> 1) & 1))) break;
