@@ -216,3 +216,20 @@ def test_attention_waits_that_run_out(nv, max_q, D):
     assert nv.device_status() == 0
     with pytest.raises(nv.NVFP4Error):
         nv.selftest_attention_timeout(q, cache, *args, timeout_ns=0)
+
+
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_attention_of_thousands_of_sequences_with_prompts_among_them(nv, max_q):
+    # prompts of many tiles in front of the 256th sequence and behind it, and far behind
+    rng = np.random.default_rng(23)
+    n, D, page = 3000, 64, 16
+    new = np.ones(n, int)
+    new[[3, 290, 2500]] = [700, 900, 400]
+    new[rng.integers(0, n, 200)] = 0
+    lens = new + rng.integers(0, 20, n)
+    q, qn, cache, pages, table = problem(nv, rng, D, page, 2, 1, new.tolist(), lens.tolist(), 0.07)
+    cu = cumulative(new.tolist())
+    out, lse = nv.paged_attention(q, cache, ints(table), ints(cu), ints(lens.tolist()), max_q=max_q, want_lse=True)
+    assert nv.device_status() == 0
+    ref = kv.attention(qn, pages, table, cu, lens.tolist(), KG, 0.07, page, D ** -0.5, True, 0)
+    compare(out, lse, ref, D)
