@@ -111,10 +111,10 @@ NVFP4_DEVINL int32_t slot_len(const PoolIndex& p, int32_t slot, int* status) {
 // Entry j of child i's row of the table: a shared page counted once more, or the
 // part page's copy.
 NVFP4_DEVINL void fork_entry(const PoolIndex& p, int a, int c, int to, int64_t j, int* status) {
-  const int64_t full = p.seq_len[c] / p.page, entries = (int64_t)p.slots * p.width;
+  const int64_t full = p.seq_len[c] / p.page;
   if (j > full || (j == full && to < 0)) return;
-  if (!NVFP4_IN_BOUNDS(j, p.width, status) || !NVFP4_IN_BOUNDS((int64_t)a * p.width + j, entries, status) ||
-      !NVFP4_IN_BOUNDS((int64_t)c * p.width + j, entries, status))
+  if (!NVFP4_IN_BOUNDS(j, p.width, status) || !NVFP4_IN_BOUNDS(a, p.slots, status) ||
+      !NVFP4_IN_BOUNDS(c, p.slots, status))
     return;
   if (j < full) {
     const int64_t page = p.table[(int64_t)a * p.width + j];

@@ -233,3 +233,16 @@ def test_attention_of_thousands_of_sequences_with_prompts_among_them(nv, max_q):
     assert nv.device_status() == 0
     ref = kv.attention(qn, pages, table, cu, lens.tolist(), KG, 0.07, page, D ** -0.5, True, 0)
     compare(out, lse, ref, D)
+
+
+@pytest.mark.parametrize("max_q", [None, 1, 64])
+def test_a_batch_without_new_tokens_leaves_everything(nv, max_q):
+    # every row behind the last sequence (a padded batch that has run empty), a few sequences and many
+    for n in (3, 70):
+        q, _, cache, pages, table = problem(nv, np.random.default_rng(24), 64, 16, 4, 2, [1] * n, [40] * n, 0.07)
+        args = (ints(table), ints([0] * (n + 1)), ints([40] * n))
+        out, lse = torch.full_like(q, 5.0), torch.full(q.shape[:2], 6.0, device="cuda")
+        nv.paged_attention(q, cache, *args, out=out, lse_out=lse, max_q=max_q)
+        nv.kv_append(cache, q[:, :2], q[:, 2:], *args)
+        assert (out == 5.0).all() and (lse == 6.0).all() and np.array_equal(to_np(cache.pages), pages)
+        assert nv.device_status() == 0
