@@ -347,7 +347,8 @@ nvfp4_status nvfp4_quantize_noalloc(const void* x, int64_t M, int64_t K, nvfp4_m
  * Lengths, offsets and tables are read on the device when the kernels run, so a
  * captured graph can be replayed with other values. A negative, decreasing or
  * too large offset or length, or a page outside the pool, is recorded as
- * NVFP4_ERR_PAGE and its tokens are skipped (appending) or masked (attention).
+ * NVFP4_ERR_PAGE and its tokens are skipped (appending) or masked (attention);
+ * rows between malformed offsets belong to no sequence.
  * Rows before cu_q[0] and at or behind cu_q[batch] belong to no sequence: their
  * results are not written.
  */
@@ -384,7 +385,10 @@ size_t nvfp4_paged_attention_workspace_bytes(void);
  *   t - j < window if window > 0. Query head h reads KV head
  *   h / (q_heads / kv_heads). Products of FP16 operands (cached values exact,
  *   queries exact to 2^-29 of their row's largest, softmax weights rounded to
- *   FP16), sums and softmax statistics in FP32, out rounded once to BF16.
+ *   FP16, with the row's largest at 2^7 to 2^15), sums and softmax statistics in
+ *   FP32, out rounded once to BF16. A query row that holds NaN or Inf gives NaN in
+ *   its own row of out and lse (zeros and -Inf if all its scores are -Inf), however
+ *   the work is divided, and leaves the others bit for bit.
  * q           BF16 [total][q_heads][head_dim], 16-byte aligned, rows q_stride
  *             elements apart (a multiple of 8).
  * max_q       the most new tokens of any sequence, as the caller knows it: it

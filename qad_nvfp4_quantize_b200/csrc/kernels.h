@@ -96,7 +96,7 @@ cudaError_t launch_moe(const MoeArgs& a, int* status, int num_sms, cudaStream_t 
 // launches it (`done`: a word of the kernel's own, a bit for each device).
 cudaError_t allow_dynamic_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
-// Paged NVFP4 KV cache (kv_append.cu, kv_pages.cu, kv_attention.cu).
+// Paged NVFP4 KV cache (kv_append.cu, kv_pages.cu, kv_attention.cu, kv_prefill.cu).
 struct KvIndex;
 struct AttnArgs;
 cudaError_t launch_kv_append(const void* k, const void* v, int64_t stride, int D, const KvIndex& ix, uint8_t* pages,

@@ -9,8 +9,8 @@
 // for single tokens. A lane takes one 16-element block at a time (32 B read, 8 B
 // of codes written) of a warp's consecutive tokens, the next one's loads in
 // flight meanwhile; the sequence is looked up once and then followed. Measured, 8
-// KV heads of 128: 28,316 tokens in MAX 39 us (3.8 TB/s; 5 TB/s for the part that
-// grows with the tokens), in FOUR_OVER_SIX 57 us; 64 single tokens 8 us.
+// KV heads of 128, single calls on a cold cache: 30,305 tokens (159 MB) in MAX 43
+// us (3.7 TB/s), in FOUR_OVER_SIX 63 us (59 back to back); 64 single tokens 8 us.
 #include <type_traits>
 
 #include "kernels.h"

@@ -1,5 +1,5 @@
 // Layout and index arithmetic of the paged NVFP4 KV cache (kv_append.cu,
-// kv_pages.cu, kv_attention.cu). The storage follows "Developing Nemotron 3.5
+// kv_pages.cu, kv_attention.cu, kv_prefill.cu). The storage follows "Developing Nemotron 3.5
 // Lightning NVFP4 with QAD using NVIDIA Model Optimizer", Table 1
 // "four_over_six + NVFP4 KV": K and V in NVFP4 (blocks of 16 along the head
 // dimension, one static FP32 global scale each), attention in 16-bit floating

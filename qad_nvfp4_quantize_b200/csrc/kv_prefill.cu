@@ -3,11 +3,12 @@
 //
 // Bound: the tensor pipe (4*D FLOP per row and token), the 2^x unit (16 a cycle
 // and SM: as long as the two MMAs of a 128 x 128 tile with D = 128) and the
-// issue slots that dequantization and softmax share. Measured, 32 heads over 8 KV
-// heads of 128: 4,096 tokens over 12,288 cached ones (687 GFLOP) in 650 us, 1.06
-// PFLOP/s; 4 chunks of 512 over 16,384 (315 GFLOP) in 343 us. Shared memory is
-// then 76 % busy (49 % the MMAs' operands, 28 % loads and stores), the tensor
-// pipe 49 % and the issue slots 50 %.
+// issue slots that dequantization and softmax share. Measured, 32 heads of 128:
+// 4,096 tokens over 12,288 cached ones, 4 KV heads (687 GFLOP), in 645 to 680 us by
+// itself (up to 1.06 PFLOP/s), 705 to 713 back to back under the power limit; 4
+// chunks of up to 512 over 16,384, 8 KV heads (315 GFLOP), in 338 to 356 us. Shared
+// memory is then 76 % busy (49 % the MMAs' operands, 27 % loads and stores), the
+// tensor pipe 50 % and the issue slots 52 %.
 //
 // One CTA per SM walks its part of the work list; a work is 256 query rows (two
 // tiles of 128) of one KV head against its cached tokens, 128 at a time.
@@ -47,7 +48,13 @@ constexpr int kUnitGranules = kTileTokens / kGranule;
 // 673 us, one of eight 660, of six 651, of four 684, of two 751.
 constexpr int kPolyEvery = 6;
 
-// Of the work list (find_part), in tiles of 128 tokens.
+// Costs of the work list (find_part) in the time of a tile of 128 tokens: joining p pieces 3 + p / 2; a piece besides its
+// tiles 2 (kHead of the call); runs of at most 16 tiles are not cut (4 and 64 as the limit gave the same times within 1 %).
+// Measured, 32 heads over 8 KV heads of 128, with joins for nothing, as they are here, and at four times that: 16 tokens
+// over 4,000 49, 37 and 34 us, over 16,000 62, 56 and 56; 16 sequences of 64 tokens over up to 2,000 71, 71 and 53; 512
+// tokens over 4,000 72 each; 4 chunks of up to 512 over 16,384 336, 337 and 337. A piece at 1, 2 and 8: 16 sequences of 64
+// 70, 71 and 52; 512 over 4,000 71, 72 and 62; 2,048 over 8,000 248, 249 and 253; 64 over 16,000, four of them, 102, 104
+// and 107. No pair is best at all of these.
 struct PreCost {
   static constexpr float kSparse = 1.0f;
   static NVFP4_DEVINL float join(float pieces) { return 3.0f + 0.5f * pieces; }
@@ -205,7 +212,8 @@ NVFP4_DEVINL f32x2 add2(f32x2 a, f32x2 b) {
 }
 // 2^x of two numbers x < 128 (x <= 15 here) on the FMA pipe: n = x rounded to an integer (by
 // adding 1.5 * 2^23), a polynomial for 2^(x - n) on [-1/2, 1/2], n added to the
-// exponent. Its coefficients are a relative minimax fit of degree 5 (least
+// exponent (the reduction of Cody and Waite, "Software Manual for the Elementary
+// Functions", 1980). Its coefficients are a relative minimax fit of degree 5 (least
 // squares, reweighted): off by at most 2^-22 when evaluated in FP32. Arguments
 // below -126 give 2^-126, which FP16 rounds to zero.
 NVFP4_DEVINL void exp2_poly(f32x2 x, float& r0, float& r1) {
