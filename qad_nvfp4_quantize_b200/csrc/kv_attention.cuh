@@ -65,12 +65,12 @@ NVFP4_DEVINL float max3_nan(float a, float b, float c) {
 }
 
 // Power of two that brings a row of BF16 queries whose largest magnitude is
-// amax to [2^14, 2^15), as the exponent to add (0 for a zero or non-finite
-// row). FP16 then holds every query exactly down to 2^-29 of the row's largest,
+// amax to [2^14, 2^15), as the exponent to add (0 for a non-finite row; a zero
+// or subnormal one gets the largest). FP16 then holds every query exactly down to 2^-29 of the row's largest,
 // and to 2^-40 of it below.
 NVFP4_DEVINL int query_exponent(float amax) {
   const int e = (int)((__float_as_uint(amax) >> 23) & 0xFFu);
-  return e == 0 || e == 255 ? 0 : 14 + 127 - e;
+  return e == 255 ? 0 : 14 + 127 - (e > 0 ? e : 1);
 }
 // x * 2^e for |e| up to 140 (two exact factors; a subnormal x stays one).
 NVFP4_DEVINL float scale_exp2(float x, int e) {

@@ -246,3 +246,18 @@ def test_a_batch_without_new_tokens_leaves_everything(nv, max_q):
         nv.kv_append(cache, q[:, :2], q[:, 2:], *args)
         assert (out == 5.0).all() and (lse == 6.0).all() and np.array_equal(to_np(cache.pages), pages)
         assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_zero_and_subnormal_queries(nv, max_q):
+    # a row's power of two is taken out before FP16 down to BF16's smallest numbers; a query of zeros weighs all alike
+    D, page, new, lens = 128, 16, [2, 20], [70, 50]
+    for value in (2.0 ** -130, 2.0 ** -126, 0.0):
+        q, _, cache, pages, table = problem(nv, np.random.default_rng(25), D, page, 4, 2, new, lens, 0.07)
+        q = (q.float() * value).to(torch.bfloat16)
+        out, lse = nv.paged_attention(q, cache, ints(table), ints(cumulative(new)), ints(lens), scale=2.0 ** 126,
+                                      max_q=max_q, want_lse=True)
+        ref = kv.attention(bf16_np(q), pages, table, cumulative(new), lens, KG, 0.07, page, 2.0 ** 126, True, 0)
+        assert value == 0.0 or np.ptp(ref["lse"]) > 0.1
+        compare(out, lse, ref, D)
+        assert nv.device_status() == 0
