@@ -85,6 +85,7 @@ struct AttnShared {
   uint64_t bar[kAttnWarps][kStages];
   float wm[kAttnWarps][kRows], wl[kAttnWarps][kRows];
   float m[kRows], l[kRows];
+  float factor[kAttnWarps][kRows];  // of warps with a row of huge scores
   int last;
   volatile int abort;
 };
@@ -240,6 +241,22 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
         }
       }
     }
+    bool huge = false;  // some row's scores are multiplied by its factor before the maximum, not with it
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) huge |= factor[nt][0] > kHugeFactor<D> || factor[nt][1] > kHugeFactor<D>;
+    huge = __any_sync(0xFFFFFFFFu, huge);
+    if (huge) {
+      __syncwarp();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const bool of_row = factor[nt][c] > kHugeFactor<D>;
+          sh.factor[warp][8 * nt + 2 * t + c] = of_row ? factor[nt][c] : 1.0f;
+          if (of_row) factor[nt][c] = 1.0f;
+        }
+      __syncwarp();
+    }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       all_lo = max(all_lo, __shfl_xor_sync(0xFFFFFFFFu, all_lo, o));
@@ -337,6 +354,18 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
               const int tk = tok0 + kGranule * y + token_of(g + (e & 2) * 4), c = e & 1;
               if (tk < lo[nt][c] || tk >= hi[nt][c] || !((two >> y) & 1u)) s[nt][y][e] = -INFINITY;
             }
+      }
+      if (huge) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float f = sh.factor[warp][8 * nt + 2 * t + c];
+            s[nt][0][c] *= f;
+            s[nt][0][c + 2] *= f;
+            s[nt][1][c] *= f;
+            s[nt][1][c + 2] *= f;
+          }
       }
       float top[NT][2];
 #pragma unroll

@@ -142,12 +142,17 @@ constexpr int64_t kAttnWaitCycles = 4000000000ll;  // about 2 s
 // 11 bits down to 2^-14 and multiples of 2^-24 below. Without the head-room tokens 16 nats below an attention sink lost
 // their weights, and those more than 17.3 below it vanished from the output.
 constexpr float kRescaleAt = 8.0f, kHeadroom = 7.0f;
-constexpr float kStartMax = -1e30f;                // running maximum before the first visible token
+constexpr float kStartMax = -3.40282347e38f;       // running maximum before the first visible token
+// A weight is 2^(s * factor - m) by one FMA: the product is not rounded, m is, by half a step of the score. From 2^24 on
+// that can lift a weight above FP16, from 2^28 on every largest one. A row whose factor would let its scores (at most D
+// products of 2^15 and 11.25) reach 2^22 has them multiplied first, rounded as m is.
+template <int D>
+constexpr float kHugeFactor = 4194304.0f / (D * 368640.0f);
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 // A row whose largest new score is `top` keeps its running maximum m, whatever
 // its neighbours do, or takes a new one where top exceeds m by more.
-NVFP4_DEVINL bool exceeds(float top, float m) { return top > m + (kRescaleAt + kHeadroom); }
+NVFP4_DEVINL bool exceeds(float top, float m) { return top - m > kRescaleAt + kHeadroom; }
 NVFP4_DEVINL float new_max(float top, float m) { return exceeds(top, m) ? top - kHeadroom : m; }
 
 // The same value in every lane, in a form that the compiler knows to be uniform.

@@ -77,6 +77,7 @@ struct PreShared {
   uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], group[2], drain[2];
   Part<kPreRows> part;
   WorkCursor<kPreRows> cursor[kPreThreads / 32];  // one per warp: no register is spent on it
+  float factor[kPreRows];  // of warps with a row of huge scores
   uint32_t tmem;
   int last[2];
   volatile int abort;
@@ -367,7 +368,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
 
         // ---- limits of this row and of the row tile
         // not zero: a masked score is -Inf before it is multiplied
-        const float factor = fmaxf(scale_exp2(a.scale * kg * kLog2e, kValueExp - ex), 1.17549435e-38f);
+        float factor = fmaxf(scale_exp2(a.scale * kg * kLog2e, kValueExp - ex), 1.17549435e-38f);
+        const bool of_row = factor > kHugeFactor<D>, huge = __any_sync(0xFFFFFFFFu, of_row);
+        if (huge) sh.factor[tid] = of_row ? factor : 1.0f;  // a row's scores are multiplied before the maximum, not with it
+        if (of_row) factor = 1.0f;
         const int64_t pos0 = (int64_t)w.seq.len - w.seq.rows;
         const int32_t r_last = (nrows - r0 < 128 ? nrows : r0 + 128) - 1;
         const Visible first_row = visible(pos0 + a.by_group.divide(r0), w.seq.len, a.causal, a.window);
@@ -410,6 +414,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           }
           uint32_t y[64];
           tmem_read64(t_x, y);
+          if (huge) {
+            const float f = sh.factor[tid];
+#pragma unroll
+            for (int e = 0; e < 64; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+          }
           float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
 #pragma unroll
           for (int e = 0; e < 64; e += 8) {
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
             t3 = max3_nan(t3, __uint_as_float(y[e + 6]), __uint_as_float(y[e + 7]));
           }
           const float top = max3_nan(max2_nan(t0, t1), t2, t3) * factor;
-          if (__any_sync(0xFFFFFFFFu, !(top <= m + (kRescaleAt + kHeadroom)))) {
+          if (__any_sync(0xFFFFFFFFu, !(top - m <= kRescaleAt + kHeadroom))) {
             // (a score of NaN or +Inf stays in m: the sum would not show it where exp2_poly has its place)
             const float m1 = top < INFINITY ? new_max(top, m) : NAN;
             const float f = m == kStartMax ? 0.0f : ex2(m - m1);

@@ -261,3 +261,46 @@ def test_zero_and_subnormal_queries(nv, max_q):
         assert value == 0.0 or np.ptp(ref["lse"]) > 0.1
         compare(out, lse, ref, D)
         assert nv.device_status() == 0
+
+
+# -------------------------------------------------------------- huge scores
+@pytest.mark.parametrize("power", [0, 10, 18, 20, 21, 22, 23, 24, 26, 30, 60, 110])
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_scores_of_any_size_pick_the_largest(nv, max_q, power):
+    """Queries up to 2^110: the softmax of scores that lie far apart is one at the largest, whatever their size."""
+    D, page, heads = 128, 64, 2
+    rng = np.random.default_rng(power)
+    for new, L in ((1, 200), (3, 60000)):
+        sign = np.where(rng.random((1, heads, D)) < 0.5, -1.0, 1.0)
+        size = rng.choice([0.25, 0.5, 1.0, 1.25], (L, heads, 1))
+        best = rng.integers(0, L - new, heads)
+        size[best, np.arange(heads)] = 2.0
+        k = torch.from_numpy((sign * size).astype(np.float32)).to(torch.bfloat16).cuda()
+        v = torch.from_numpy(rng.uniform(0.5, 1.0, (L, heads, D)).astype(np.float32)).to(torch.bfloat16).cuda()
+        kg, vg = 0.001, 0.0005
+        cache = nv.kv_cache(-(-L // page), heads, D, page, *scalars(kg, vg))
+        row = rng.permutation(cache.pages.shape[0])[None]
+        nv.kv_append(cache, k, v, ints(row), ints([0, L]), ints([L]))
+        K, V = kv.gather(to_np(cache.pages), row[0], L, page, D, kg, vg)
+        q = torch.from_numpy(np.repeat(sign * 2.0 ** power, new, 0).astype(np.float32)).to(torch.bfloat16).cuda()
+        for flip in (1.0, -1.0):
+            # the opposite query: all scores are negative, the smallest keys win (many of them, all alike)
+            out, lse = nv.paged_attention(q * flip, cache, ints(row), ints([0, new]), ints([L]), max_q=max_q, want_lse=True)
+            for h in range(heads):
+                s = D ** -0.5 * 2.0 ** power * flip * (K[h] @ sign[0, h])
+                top = s.max()
+                for t in range(new):
+                    see = s[:L - new + t + 1]
+                    p = np.exp(see - top)
+                    want, mass = p @ V[h, :len(see)] / p.sum(), top + np.log(p.sum())
+                    # A score is off by at most e_s (kv.attention_tolerance). From queries of 2^10 on two different ones lie
+                    # 0.25 * 2^10 * sqrt(D) nats or more apart, far beyond e_s: all but the largest vanish, and those of
+                    # equal keys are equal. Weights are rounded to FP16 (2^-11), the sums add (n + 64) * 2^-24 each, the
+                    # output is rounded to BF16; its values lie below 1.
+                    e_s = (D + 16) * 2.0 ** -24 * np.abs(see).max() + 2.0 ** -21
+                    rel = (2 * e_s if power < 10 else 0.0) + 2.0 ** -11 + 2 * (len(see) + 64) * 2.0 ** -24
+                    err = np.abs(bf16_np(out)[t, h] - want)
+                    assert (err <= 2.0 ** -8 * np.abs(want) + rel * (1 + 2.0 ** -8)).all(), (power, flip, err.max())
+                    got = float(lse[t, h])
+                    assert abs(got - mass) <= e_s + (len(see) + 64) * 2.0 ** -24 + 2.0 ** -21 * (abs(mass) + 1), (got, mass)
+    assert nv.device_status() == 0
