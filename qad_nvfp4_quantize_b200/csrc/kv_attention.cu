@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm<D, NT>) kv_attention_
       if (r >= nrows) return;
       const int32_t tok = a.by_group.divide(r), hq = head * a.group + r - tok * a.group;
       const int64_t at = (seq.row0 + tok) * a.ix.hkv * a.group + hq;
-      const float f = x.l == 0.0f ? 0.0f : kValueScale * vg / x.l;  // no visible token: zeros
+      const float f = x.l == 0.0f ? 0.0f : output_factor(vg, x.l);  // no visible token: zeros
       if (!NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status)) return;
       *reinterpret_cast<uint2*>(a.out + at * D + d) =
           make_uint2(f32x2_to_bf16x2(x.o.x * f, x.o.y * f), f32x2_to_bf16x2(x.o.z * f, x.o.w * f));

@@ -36,7 +36,8 @@ NVFP4_DEVINL void codes_to_half(uint32_t w, uint32_t (&p)[4]) {
 }
 
 constexpr int kValueExp = 8;            // cached values are held as k, v / g * 2^-8
-constexpr float kValueScale = 256.0f;
+// What O / l is multiplied by: 2^8 * g, in an order that passes FP32's range only where the output does.
+NVFP4_DEVINL float output_factor(float vg, float l) { return 256.0f / l * vg; }
 
 // Two E4M3 scales (low bytes of each half) -> FP16 pair s * 2^-8.
 NVFP4_DEVINL uint32_t scales_to_half(uint32_t two) { return (two & 0x007F007Fu) << 7; }

@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         const bool write = live && NVFP4_IN_BOUNDS(at, a.ix.total * a.ix.hkv * a.group, a.status);
         if (whole_work) {
           // (by the maximum: l of a row that saw nothing holds the 2^-126 that exp2_poly gives for a masked score)
-          const float f = m == -INFINITY ? 0.0f : kValueScale * vg / l;
+          const float f = m == -INFINITY ? 0.0f : output_factor(vg, l);
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
               const float mc = __ldcg(part_of(c, c == c0) + row);
               lt += mc == -INFINITY ? 0.0f : __ldcg(part_of(c, c == c0) + 128 + row) * ex2(mc - mt);
             }
-            const float f = lt == 0.0f ? 0.0f : kValueScale * vg / lt;
+            const float f = lt == 0.0f ? 0.0f : output_factor(vg, lt);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               float o[32];

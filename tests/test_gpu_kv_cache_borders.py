@@ -304,3 +304,17 @@ def test_scores_of_any_size_pick_the_largest(nv, max_q, power):
                     got = float(lse[t, h])
                     assert abs(got - mass) <= e_s + (len(see) + 64) * 2.0 ** -24 + 2.0 ** -21 * (abs(mass) + 1), (got, mass)
     assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("vg", [2.0 ** -120, 2.0 ** -100, 2.0 ** 100, 2.0 ** 120])
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_value_scales_near_the_ends_of_fp32(nv, max_q, vg):
+    # outputs that BF16 holds come out whatever the global scale, from whole works and from parts
+    for new, lens in (([3, 20], [70, 50]), ([1, 2], [40000, 9])):
+        D, page = 128, 64
+        q, qn, cache, pages, table = problem(nv, np.random.default_rng(26), D, page, 4, 2, new, lens, vg)
+        cu = cumulative(new)
+        out, lse = nv.paged_attention(q, cache, ints(table), ints(cu), ints(lens), max_q=max_q, want_lse=True)
+        ref = kv.attention(qn, pages, table, cu, lens, KG, vg, page, D ** -0.5, True, 0)
+        compare(out, lse, ref, D)
+        assert nv.device_status() == 0
