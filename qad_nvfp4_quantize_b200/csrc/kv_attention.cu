@@ -3,8 +3,8 @@
 //
 // Mathematics: one pass over the cached tokens (the running maximum and sum of
 // Milakov and Gimelshein, "Online normalizer calculation for softmax", 2018) with
-// a maximum m, sum l and unnormalised output O per query row: m' = max(m, s), O = O * 2^(m - m') +
-// 2^(s - m') v (scores in units of log2). m is held 7 below the score that set
+// a maximum m, sum l and unnormalised output O per query row: m' = max(m, s), O =
+// O * 2^(m - m') + 2^(s - m') v (scores in units of log2). m is held 7 below the score that set
 // it, and O and l are rescaled only when a score exceeds m by more than 15: a
 // row's largest p = 2^(s - m) lies between 2^7 and 2^15, FP16's upper end, and
 // the sums in FP32 lose nothing.
@@ -12,10 +12,10 @@
 // Bound: HBM, 18*D bytes per 16 tokens and KV head. The rows of one KV head
 // (all its query heads, all new tokens of the tile) share each fetched granule.
 // Measured, D = 128, 8 rows (single calls on a cold cache): 64 sequences of up to
-// 16,384 tokens (739 MB) in 153 to 158 us, 4.7 to 4.8 TB/s; 2 of 131,072 (75 MB)
-// in 33 to 35 us (29 back to back). The same loop without its arithmetic, which
-// only copies, takes 137 us, without dequantization 145; issue slots are 64 %
-// busy, the ALU 55 %. Single tokens over 1,024 cached ones take 14
+// 16,384 tokens (739 MB) in 155 to 158 us, 4.7 to 4.8 TB/s; 2 of 131,072 (75 MB)
+// in 33 to 35 us (30 back to back). The same loop without its arithmetic, which
+// only copies, takes 137 us, without dequantization 145; issue slots are 63 %
+// busy, the ALU 54 %. Single tokens over 1,024 cached ones take 14
 // us, 4 of them for lengths, page table and queries, one read behind the other,
 // and 1 us for each 32 tokens of a warp.
 //

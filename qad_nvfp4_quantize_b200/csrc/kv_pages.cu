@@ -43,8 +43,9 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* sh, int* total) 
 // ------------------------------------------------------------------ copying
 // Page src[i] -> page dst[i]; entries with a negative index are skipped. Bound
 // by HBM (each byte read and written once). A CTA copies pieces of 32 KB, eight
-// 16-byte loads in flight per thread (compacting 16,384 pages of 74 KB: 112 us
-// for the whole call on a cold cache, 107 back to back; 120 with four loads); an entry is as many pieces as its page
+// 16-byte loads in flight per thread (compacting 16,384 pages of 74 KB: 110 to
+// 112 us for the whole call on a cold cache, 107 back to back; with four loads 120
+// where this took 111); an entry is as many pieces as its page
 // needs, so a few large pages spread over the card too. Where a page is copied
 // many times the writes bound it: 151 MB take 43 us, as filling that much does.
 constexpr int kRowThreads = 256;
